@@ -44,6 +44,23 @@ SIGNATURES = {
     "h3_mixer_workspace": (_sz, [_i, _i, _i, _i, _i]),
     "h3_mixer_fwd": (_i, [_vp, _vp, _vp, _fp, _fp, _fp, _fp, _fp, _fp, _vp, _i, _i, _i, _i, _i, _i, _vp, _sz,
                           _i, _vp]),
+    "short_conv_fwd": (_i, [_vp, _fp, _fp, _vp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp]),
+    "short_conv_bwd_workspace": (_sz, [_i, _i, _i, _i]),
+    "short_conv_bwd": (_i, [_vp, _vp, _fp, _fp, _vp, _fp, _fp, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz,
+                            _i, _vp]),
+    "short_conv_step": (_i, [_vp, _vp, _fp, _fp, _vp, _i, _i, _i, _i, _vp, _i, ctypes.c_longlong, _i, _vp]),
+    "selective_scan_ckpt_bytes": (_sz, [_i, _i, _i, _i]),
+    "selective_scan_fwd": (_i, [_vp, _vp, _fp, _vp, _vp, _fp, _fp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _fp,
+                                _fp, _fp, _i, _vp]),
+    "selective_scan_bwd_workspace": (_sz, [_i, _i, _i, _i, _i]),
+    "selective_scan_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _fp, _fp, _vp, _fp, _vp, _vp, _fp, _vp, _vp, _fp, _fp,
+                                _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _fp, _fp, _vp, _sz, _i, _vp]),
+    "selective_scan_step": (_i, [_vp, _vp, _fp, _vp, _vp, _fp, _fp, _vp, _fp, _vp, _i, _i, _i, _i, _i, _vp, _i, _vp,
+                                 _i, _vp]),
+    "group_norm_act_fwd": (_i, [_vp, _fp, _fp, _vp, _vp, _i, _i, _i, _i, ctypes.c_float, _i, _i, _vp]),
+    "group_norm_act_bwd_workspace": (_sz, [_i, _i, _i, _i, _i]),
+    "group_norm_act_bwd": (_i, [_vp, _vp, _fp, _fp, _vp, _vp, _fp, _fp, _vp, _i, _i, _i, _i, ctypes.c_float, _i, _vp,
+                                _sz, _i, _vp]),
 }
 
 _lib = None

@@ -461,4 +461,358 @@ FC_API unsigned int fc_tc_timeouts(void) {
 
 FC_TEST_API unsigned int fc_debug_tc_timeouts(void) { return fc_tc_timeouts(); }
 
+
+// ------------------------------------------------------------------ selective SSM
+namespace {
+
+constexpr int kMaxSteps = 1 << 30;  // sequence length: vector offsets stay in an int
+
+// A strided input of B x R rows of `len` contiguous elements, in G groups (group stride st[1], row stride st[2]; G == 1
+// without groups: st = batch, row).  False for a negative stride or an extent past 2^60 elements.
+bool rows_of(fc::Rows* r, const void* p, const long long* st, bool grouped, int B, int G, int R, int len, int dtype) {
+  const long long lim = 1LL << 60;
+  const int per16 = 16 / (int)dtype_size(dtype);
+  r->p = p;
+  if (st) {
+    r->bs = st[0];
+    r->gs = grouped ? st[1] : 0;
+    r->rs = grouped ? st[2] : st[1];
+  } else {
+    r->rs = len;
+    r->gs = (long long)R * len;
+    r->bs = (long long)G * R * len;
+  }
+  if (r->bs < 0 || r->rs < 0 || r->gs < 0) return false;
+  if (r->bs > lim / B || r->gs > lim / G || r->rs > lim / R) return false;
+  r->vec = aligned(p, 16) && r->bs % per16 == 0 && r->rs % per16 == 0 && r->gs % per16 == 0;
+  return true;
+}
+
+// One past the last element that rows_of()'s tensor holds, in elements from its start.
+size_t rows_end(const fc::Rows& r, int B, int G, int R, int len) {
+  return (size_t)((B - 1) * r.bs + (G - 1) * r.gs + (R - 1) * r.rs + len);
+}
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const char* x = (const char*)a;
+  const char* y = (const char*)b;
+  return a && b && na && nb && x < y + nb && y < x + na;
+}
+
+fc_status check_sizes(int B, int H, int L, int dtype) {
+  FC_REQUIRE(dtype_ok(dtype), FC_EINVAL, "unknown dtype %d", dtype);
+  FC_REQUIRE(B >= 1 && H >= 1 && L >= 1, FC_EINVAL, "B, H, L must be >= 1 (got %d, %d, %d)", B, H, L);
+  FC_REQUIRE(L <= kMaxSteps, FC_EUNSUPPORTED, "L = %d > 2^30", L);
+  // grids count blocks of up to 1024 steps of a row
+  FC_REQUIRE((double)B * H * (((double)L + 1023) / 1024) < 2147483647.0, FC_EUNSUPPORTED,
+             "B * H * ceil(L / 1024) must be below 2^31");
+  return FC_OK;
+}
+
+fc_status check_step(int B, int S, const int* slots) {
+  FC_REQUIRE(B <= 65535, FC_EUNSUPPORTED, "B = %d > 65535", B);
+  FC_REQUIRE(S >= 1, FC_EINVAL, "the state pool must hold at least one row (got %d)", S);
+  FC_REQUIRE(slots || S == B, FC_EINVAL, "without slots the state has one row for each of the batch (%d, got %d)", B, S);
+  FC_REQUIRE(aligned(slots, 4), FC_EINVAL, "slots must be 4-byte aligned");
+  return FC_OK;
+}
+
+}  // namespace
+
+static fc_status check_short_conv(const void* x, const float* w, const float* bias, int B, int H, int L, int K,
+                                  int dtype) {
+  fc_status s = check_sizes(B, H, L, dtype);
+  if (s != FC_OK) return s;
+  FC_REQUIRE(K >= 1 && K <= 8, FC_EUNSUPPORTED, "K must be in [1, 8] (got %d)", K);
+  FC_REQUIRE(x && w, FC_EINVAL, "null x or w");
+  FC_REQUIRE(aligned(x, dtype_size(dtype)) && aligned(w, 4) && aligned(bias, 4), FC_EINVAL,
+             "x, w and bias must be aligned to their elements");
+  return FC_OK;
+}
+
+FC_API fc_status short_conv_fwd(const void* x, const float* w, const float* bias, void* y, int B, int H, int L, int K,
+                                int silu, const int* lengths, const long long* strides, const void* state_in,
+                                void* state_out, fc_dtype dtype, void* stream) {
+  g_err[0] = 0;
+  fc_status s = check_short_conv(x, w, bias, B, H, L, K, dtype);
+  if (s != FC_OK) return s;
+  const size_t e = dtype_size(dtype), tail = (size_t)B * H * (K - 1) * e;
+  FC_REQUIRE(y && aligned(y, 16), FC_EINVAL, "y must be non-null and 16-byte aligned");
+  FC_REQUIRE(aligned(lengths, 4) && aligned(state_in, e) && aligned(state_out, e), FC_EINVAL,
+             "lengths and states must be aligned to their elements");
+  fc::Rows xr;
+  FC_REQUIRE(rows_of(&xr, x, strides, false, B, 1, H, L, dtype), FC_EINVAL, "strides must be >= 0 and in range");
+  const size_t xe = rows_end(xr, B, 1, H, L) * e, ye = (size_t)B * H * L * e;
+  FC_REQUIRE(!overlap(x, xe, y, ye) && !overlap(state_in, tail, y, ye), FC_EINVAL, "y overlaps an input");
+  FC_REQUIRE(!overlap(x, xe, state_out, tail) && !overlap(y, ye, state_out, tail) &&
+                 !overlap(state_in, tail, state_out, tail),
+             FC_EINVAL, "state_out overlaps another array");
+  return cuda_status(fc::launch_short_conv(xr, w, bias, y, B, H, L, K, silu, lengths, K > 1 ? state_in : nullptr,
+                                           K > 1 ? state_out : nullptr, L % (16 / (int)e) == 0, dtype,
+                                           (cudaStream_t)stream),
+                     "short_conv_fwd launch");
+}
+
+FC_API size_t short_conv_bwd_workspace(int B, int H, int L, int K) {
+  if (B < 1 || H < 1 || L < 1 || K < 1 || K > 8) return 0;
+  return (size_t)fc::short_conv_bwd_splits(B, H, L) * H * (K + 1) * 4;
+}
+
+FC_API fc_status short_conv_bwd(const void* dy, const void* x, const float* w, const float* bias, void* dx, float* dw,
+                                float* dbias, int B, int H, int L, int K, int silu, const int* lengths,
+                                const long long* strides, const void* state_in, const void* dstate_out,
+                                void* dstate_in, void* workspace, size_t ws_bytes, fc_dtype dtype, void* stream) {
+  g_err[0] = 0;
+  fc_status s = check_short_conv(x, w, bias, B, H, L, K, dtype);
+  if (s != FC_OK) return s;
+  const size_t e = dtype_size(dtype), tail = (size_t)B * H * (K - 1) * e;
+  FC_REQUIRE(dy && dx && dw, FC_EINVAL, "null dy, dx or dw");
+  FC_REQUIRE(aligned(dx, 16), FC_EINVAL, "dx must be 16-byte aligned");
+  FC_REQUIRE(aligned(dy, e) && aligned(dw, 4) && aligned(dbias, 4) && aligned(lengths, 4) && aligned(state_in, e) &&
+                 aligned(dstate_out, e) && aligned(dstate_in, e),
+             FC_EINVAL, "arrays must be aligned to their elements");
+  fc::Rows xr, gr;
+  FC_REQUIRE(rows_of(&gr, dy, strides, false, B, 1, H, L, dtype) &&
+                 rows_of(&xr, x, strides ? strides + 2 : nullptr, false, B, 1, H, L, dtype),
+             FC_EINVAL, "strides must be >= 0 and in range");
+  const size_t xe = rows_end(xr, B, 1, H, L) * e, ge = rows_end(gr, B, 1, H, L) * e, oe = (size_t)B * H * L * e;
+  FC_REQUIRE(!overlap(x, xe, dx, oe) && !overlap(dy, ge, dx, oe) && !overlap(state_in, tail, dx, oe) &&
+                 !overlap(dstate_out, tail, dx, oe),
+             FC_EINVAL, "dx overlaps an input");
+  FC_REQUIRE(!overlap(x, xe, dstate_in, tail) && !overlap(dy, ge, dstate_in, tail) &&
+                 !overlap(dx, oe, dstate_in, tail) && !overlap(state_in, tail, dstate_in, tail) &&
+                 !overlap(dstate_out, tail, dstate_in, tail),
+             FC_EINVAL, "dstate_in overlaps another array");
+  const size_t need = short_conv_bwd_workspace(B, H, L, K);
+  FC_REQUIRE(workspace && aligned(workspace, 256), FC_EINVAL, "workspace must be non-null and 256-byte aligned");
+  FC_REQUIRE(ws_bytes >= need, FC_EINVAL, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  return cuda_status(
+      fc::launch_short_conv_bwd(gr, xr, w, bias, dx, dw, dbias, B, H, L, K, silu, lengths, K > 1 ? state_in : nullptr,
+                                K > 1 ? dstate_out : nullptr, K > 1 ? dstate_in : nullptr, (float*)workspace,
+                                L % (16 / (int)e) == 0, dtype, (cudaStream_t)stream),
+      "short_conv_bwd launch");
+}
+
+FC_API fc_status short_conv_step(const void* x, void* state, const float* w, const float* bias, void* y, int B, int H,
+                                 int K, int silu, const int* slots, int S, long long x_stride, fc_dtype dtype,
+                                 void* stream) {
+  g_err[0] = 0;
+  fc_status s = check_short_conv(x, w, bias, B, H, 1, K, dtype);
+  if (s != FC_OK) return s;
+  if ((s = check_step(B, S, slots)) != FC_OK) return s;
+  const size_t e = dtype_size(dtype), pool = (size_t)S * H * (K - 1) * e;
+  FC_REQUIRE(y && aligned(y, e), FC_EINVAL, "y must be non-null and aligned to its elements");
+  FC_REQUIRE(K == 1 || (state && aligned(state, e)), FC_EINVAL, "state must be non-null and aligned to its elements");
+  FC_REQUIRE(x_stride >= 0 && x_stride <= (1LL << 60) / B, FC_EINVAL, "x_stride must be >= 0 and in range");
+  const size_t xe = (size_t)((B - 1) * x_stride + H) * e, ye = (size_t)B * H * e;
+  FC_REQUIRE(!overlap(x, xe, y, ye), FC_EINVAL, "x and y overlap");
+  FC_REQUIRE(K == 1 || (!overlap(x, xe, state, pool) && !overlap(y, ye, state, pool)), FC_EINVAL,
+             "state overlaps x or y");
+  return cuda_status(fc::launch_short_conv_step(x, x_stride, state, w, bias, y, B, H, K, silu, slots, S, dtype,
+                                                (cudaStream_t)stream),
+                     "short_conv_step launch");
+}
+
+// Sizes, parameters and inputs that the scan's calls share; fills p (strides: batch and row of u, delta and z, then
+// batch, group and row of Bt and Ct).
+static fc_status scan_args(fc::ScanArgs* p, const void* u, const void* delta, const float* A, const void* Bt,
+                           const void* Ct, const float* D, const float* dt_bias, const void* z, int B, int H, int L,
+                           int N, int G, int softplus, const int* lengths, const long long* st, int dtype) {
+  fc_status s = check_sizes(B, H, L, dtype);
+  if (s != FC_OK) return s;
+  FC_REQUIRE(N >= 1 && G >= 1, FC_EINVAL, "N, G must be >= 1 (got %d, %d)", N, G);
+  FC_REQUIRE(N <= 256, FC_EUNSUPPORTED, "N = %d > 256", N);
+  FC_REQUIRE(H % G == 0, FC_EINVAL, "H = %d is not a multiple of G = %d", H, G);
+  FC_REQUIRE((double)B * G * N * L < 274877906944.0, FC_EUNSUPPORTED, "B * G * N * L must be below 2^38");
+  FC_REQUIRE(u && delta && A && Bt && Ct, FC_EINVAL, "null u, delta, A, Bt or Ct");
+  const size_t e = dtype_size(dtype);
+  FC_REQUIRE(aligned(u, e) && aligned(delta, e) && aligned(z, e) && aligned(Bt, e) && aligned(Ct, e) &&
+                 aligned(A, 4) && aligned(D, 4) && aligned(dt_bias, 4) && aligned(lengths, 4),
+             FC_EINVAL, "arrays must be aligned to their elements");
+  *p = fc::ScanArgs{};
+  FC_REQUIRE(rows_of(&p->u, u, st, false, B, 1, H, L, dtype) &&
+                 rows_of(&p->delta, delta, st ? st + 2 : nullptr, false, B, 1, H, L, dtype) &&
+                 rows_of(&p->z, z, st ? st + 4 : nullptr, false, B, 1, H, L, dtype) &&
+                 rows_of(&p->Bt, Bt, st ? st + 6 : nullptr, true, B, G, N, L, dtype) &&
+                 rows_of(&p->Ct, Ct, st ? st + 9 : nullptr, true, B, G, N, L, dtype),
+             FC_EINVAL, "strides must be >= 0 and in range");
+  p->A = A;
+  p->D = D;
+  p->dt_bias = dt_bias;
+  p->lengths = lengths;
+  p->B = B;
+  p->H = H;
+  p->L = L;
+  p->N = N;
+  p->G = G;
+  p->softplus = softplus;
+  p->out_vec = L % (16 / (int)e) == 0;
+  return FC_OK;
+}
+
+// Whether [q, q + bytes) touches one of the scan's B x H x L or B x G x N x L inputs.
+static bool hits_scan_input(const fc::ScanArgs& p, size_t e, const void* q, size_t bytes) {
+  return overlap(p.u.p, rows_end(p.u, p.B, 1, p.H, p.L) * e, q, bytes) ||
+         overlap(p.delta.p, rows_end(p.delta, p.B, 1, p.H, p.L) * e, q, bytes) ||
+         overlap(p.z.p, rows_end(p.z, p.B, 1, p.H, p.L) * e, q, bytes) ||
+         overlap(p.Bt.p, rows_end(p.Bt, p.B, p.G, p.N, p.L) * e, q, bytes) ||
+         overlap(p.Ct.p, rows_end(p.Ct, p.B, p.G, p.N, p.L) * e, q, bytes);
+}
+
+FC_API size_t selective_scan_ckpt_bytes(int B, int H, int L, int N) {
+  if (B < 1 || H < 1 || L < 1 || N < 1) return 0;
+  return (size_t)B * H * (((size_t)L + fc::kCkptSteps - 1) / fc::kCkptSteps) * N * 4;
+}
+
+FC_API fc_status selective_scan_fwd(const void* u, const void* delta, const float* A, const void* Bt, const void* Ct,
+                                    const float* D, const float* dt_bias, const void* z, void* y, int B, int H, int L,
+                                    int N, int G, int softplus, const int* lengths, const long long* strides,
+                                    const float* state_in, float* state_out, float* ckpt, fc_dtype dtype,
+                                    void* stream) {
+  g_err[0] = 0;
+  fc::ScanArgs p;
+  fc_status s = scan_args(&p, u, delta, A, Bt, Ct, D, dt_bias, z, B, H, L, N, G, softplus, lengths, strides, dtype);
+  if (s != FC_OK) return s;
+  FC_REQUIRE(y && aligned(y, 16), FC_EINVAL, "y must be non-null and 16-byte aligned");
+  FC_REQUIRE(aligned(state_in, 4) && aligned(state_out, 4) && aligned(ckpt, 4), FC_EINVAL,
+             "states must be 4-byte aligned");
+  p.state_in = state_in;
+  const size_t e = dtype_size(dtype), ye = (size_t)B * H * L * e, se = (size_t)B * H * N * 4;
+  const size_t ce = selective_scan_ckpt_bytes(B, H, L, N);
+  FC_REQUIRE(!hits_scan_input(p, e, y, ye) && !overlap(state_in, se, y, ye), FC_EINVAL, "y overlaps an input");
+  FC_REQUIRE(!hits_scan_input(p, e, state_out, se) && !overlap(y, ye, state_out, se) &&
+                 !overlap(state_in, se, state_out, se),
+             FC_EINVAL, "state_out overlaps another array");
+  FC_REQUIRE(!hits_scan_input(p, e, ckpt, ce) && !overlap(y, ye, ckpt, ce) && !overlap(state_in, se, ckpt, ce) &&
+                 !overlap(state_out, se, ckpt, ce),
+             FC_EINVAL, "ckpt overlaps another array");
+  return cuda_status(fc::launch_selective_scan(p, y, state_out, ckpt, dtype, (cudaStream_t)stream),
+                     "selective_scan_fwd launch");
+}
+
+FC_API size_t selective_scan_bwd_workspace(int B, int H, int L, int N, int G) {
+  if (B < 1 || H < 1 || L < 1 || N < 1 || G < 1 || H % G) return 0;
+  return fc::selective_scan_bwd_workspace_bytes(B, H, L, N, G);
+}
+
+FC_API fc_status selective_scan_bwd(const void* dy, const void* u, const void* delta, const float* A, const void* Bt,
+                                    const void* Ct, const float* D, const float* dt_bias, const void* z,
+                                    const float* ckpt, void* du, void* ddelta, float* dA, void* dB, void* dC, float* dD,
+                                    float* ddt_bias, void* dz, int B, int H, int L, int N, int G, int softplus,
+                                    const int* lengths, const long long* strides, const float* dstate_out,
+                                    float* dstate_in, void* workspace, size_t ws_bytes, fc_dtype dtype, void* stream) {
+  g_err[0] = 0;
+  fc::ScanArgs p;
+  fc_status s = scan_args(&p, u, delta, A, Bt, Ct, D, dt_bias, z, B, H, L, N, G, softplus, lengths,
+                          strides ? strides + 2 : nullptr, dtype);
+  if (s != FC_OK) return s;
+  const size_t e = dtype_size(dtype);
+  FC_REQUIRE(dy && ckpt && du && ddelta && dA && dB && dC, FC_EINVAL, "null dy, ckpt, du, ddelta, dA, dB or dC");
+  FC_REQUIRE((z == nullptr) == (dz == nullptr), FC_EINVAL, "z and dz must both be given or both be null");
+  FC_REQUIRE(aligned(du, 16) && aligned(ddelta, 16) && aligned(dz, 16), FC_EINVAL,
+             "du, ddelta and dz must be 16-byte aligned");
+  FC_REQUIRE(aligned(dy, e) && aligned(dB, e) && aligned(dC, e) && aligned(ckpt, 4) && aligned(dA, 4) &&
+                 aligned(dD, 4) && aligned(ddt_bias, 4) && aligned(dstate_out, 4) && aligned(dstate_in, 4),
+             FC_EINVAL, "arrays must be aligned to their elements");
+  FC_REQUIRE(rows_of(&p.dy, dy, strides, false, B, 1, H, L, dtype), FC_EINVAL, "strides must be >= 0 and in range");
+  const size_t ge = rows_end(p.dy, B, 1, H, L) * e, oe = (size_t)B * H * L * e, be = (size_t)B * G * N * L * e;
+  const struct { const void* q; size_t n; } out[] = {{du, oe}, {ddelta, oe}, {dz, oe}, {dB, be}, {dC, be}};
+  for (int i = 0; i < 5; ++i) {
+    FC_REQUIRE(!hits_scan_input(p, e, out[i].q, out[i].n) && !overlap(dy, ge, out[i].q, out[i].n), FC_EINVAL,
+               "a gradient overlaps an input");
+    for (int j = 0; j < i; ++j)
+      FC_REQUIRE(!overlap(out[j].q, out[j].n, out[i].q, out[i].n), FC_EINVAL, "two gradients overlap");
+  }
+  const size_t need = selective_scan_bwd_workspace(B, H, L, N, G);
+  FC_REQUIRE(workspace && aligned(workspace, 256), FC_EINVAL, "workspace must be non-null and 256-byte aligned");
+  FC_REQUIRE(ws_bytes >= need, FC_EINVAL, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  return cuda_status(fc::launch_selective_scan_bwd(p, ckpt, du, ddelta, dA, dB, dC, dD, ddt_bias, dz, dstate_out,
+                                                   dstate_in, workspace, dtype, (cudaStream_t)stream),
+                     "selective_scan_bwd launch");
+}
+
+FC_API fc_status selective_scan_step(const void* u, const void* delta, const float* A, const void* Bt, const void* Ct,
+                                     const float* D, const float* dt_bias, const void* z, float* state, void* y, int B,
+                                     int H, int N, int G, int softplus, const int* slots, int S,
+                                     const long long* strides, fc_dtype dtype, void* stream) {
+  g_err[0] = 0;
+  fc::ScanArgs p;
+  fc_status s =
+      scan_args(&p, u, delta, A, Bt, Ct, D, dt_bias, z, B, H, 1, N, G, softplus, nullptr, strides, dtype);
+  if (s != FC_OK) return s;
+  if ((s = check_step(B, S, slots)) != FC_OK) return s;
+  const size_t e = dtype_size(dtype), ye = (size_t)B * H * e, pool = (size_t)S * H * N * 4;
+  FC_REQUIRE(y && aligned(y, e), FC_EINVAL, "y must be non-null and aligned to its elements");
+  FC_REQUIRE(state && aligned(state, 4), FC_EINVAL, "state must be non-null and 4-byte aligned");
+  FC_REQUIRE(!hits_scan_input(p, e, y, ye), FC_EINVAL, "y overlaps an input");
+  FC_REQUIRE(!hits_scan_input(p, e, state, pool) && !overlap(y, ye, state, pool), FC_EINVAL,
+             "state overlaps another array");
+  return cuda_status(fc::launch_selective_scan_step(p, state, y, slots, S, dtype, (cudaStream_t)stream),
+                     "selective_scan_step launch");
+}
+
+// ------------------------------------------------------------------ group norm with SiLU
+static fc_status check_norm(const void* x, const float* w, const float* bias, const void* gate, int B, int L, int C,
+                            int G, float eps, int dtype) {
+  fc_status s = check_sizes(B, C, L, dtype);
+  if (s != FC_OK) return s;
+  FC_REQUIRE(G >= 1 && C % G == 0, FC_EINVAL, "C = %d is not a multiple of G = %d", C, G);
+  FC_REQUIRE(C / G <= 8192, FC_EUNSUPPORTED, "C / G = %d > 8192", C / G);
+  FC_REQUIRE(G <= 65535 && C <= (1 << 28), FC_EUNSUPPORTED, "G = %d > 65535 or C = %d > 2^28", G, C);
+  FC_REQUIRE((double)B * L * G < 2147483647.0, FC_EUNSUPPORTED, "B * L * G must be below 2^31");
+  FC_REQUIRE(eps > 0.f, FC_EINVAL, "eps must be > 0");
+  FC_REQUIRE(x && aligned(x, 16) && aligned(gate, 16), FC_EINVAL, "x must be non-null, x and gate 16-byte aligned");
+  FC_REQUIRE(aligned(w, 4) && aligned(bias, 4), FC_EINVAL, "weight and bias must be 4-byte aligned");
+  return FC_OK;
+}
+
+// Whether the rows of a call (a group of a token, or a channel's tokens) start on 16-byte boundaries.
+static int norm_vec(int L, int C, int G, int channel_major, size_t e) {
+  return (channel_major ? L : C / G) * e % 16 == 0;
+}
+
+FC_API fc_status group_norm_act_fwd(const void* x, const float* weight, const float* bias, const void* gate, void* y,
+                                    int B, int L, int C, int G, float eps, int channel_major, fc_dtype dtype,
+                                    void* stream) {
+  g_err[0] = 0;
+  fc_status s = check_norm(x, weight, bias, gate, B, L, C, G, eps, dtype);
+  if (s != FC_OK) return s;
+  const size_t e = dtype_size(dtype), n = (size_t)B * L * C * e;
+  FC_REQUIRE(y && aligned(y, 16), FC_EINVAL, "y must be non-null and 16-byte aligned");
+  FC_REQUIRE(!overlap(x, n, y, n) && !overlap(gate, n, y, n), FC_EINVAL, "y overlaps an input");
+  return cuda_status(fc::launch_group_norm(x, weight, bias, gate, y, B, L, C, G, eps, channel_major,
+                                           norm_vec(L, C, G, channel_major, e), dtype, (cudaStream_t)stream),
+                     "group_norm_act_fwd launch");
+}
+
+FC_API size_t group_norm_act_bwd_workspace(int B, int L, int C, int G, int channel_major) {
+  if (B < 1 || L < 1 || C < 1 || G < 1 || C % G || C / G > 8192) return 0;
+  return (size_t)fc::group_norm_bwd_splits(B, L, C, G, channel_major) * 2 * C * 4;
+}
+
+FC_API fc_status group_norm_act_bwd(const void* dy, const void* x, const float* weight, const float* bias,
+                                    const void* gate, void* dx, float* dweight, float* dbias, void* dgate, int B, int L,
+                                    int C, int G, float eps, int channel_major, void* workspace, size_t ws_bytes,
+                                    fc_dtype dtype, void* stream) {
+  g_err[0] = 0;
+  fc_status s = check_norm(x, weight, bias, gate, B, L, C, G, eps, dtype);
+  if (s != FC_OK) return s;
+  const size_t e = dtype_size(dtype), n = (size_t)B * L * C * e;
+  FC_REQUIRE(dy && dx && aligned(dy, 16) && aligned(dx, 16) && aligned(dgate, 16), FC_EINVAL,
+             "dy and dx must be non-null, dy, dx and dgate 16-byte aligned");
+  FC_REQUIRE(aligned(dweight, 4) && aligned(dbias, 4), FC_EINVAL, "dweight and dbias must be 4-byte aligned");
+  FC_REQUIRE((gate == nullptr) == (dgate == nullptr), FC_EINVAL, "gate and dgate must both be given or both be null");
+  const void* in[] = {dy, x, gate};
+  for (const void* q : in)
+    FC_REQUIRE(!overlap(q, n, dx, n) && !overlap(q, n, dgate, n), FC_EINVAL, "a gradient overlaps an input");
+  FC_REQUIRE(!overlap(dx, n, dgate, n), FC_EINVAL, "dx and dgate overlap");
+  const size_t need = group_norm_act_bwd_workspace(B, L, C, G, channel_major);
+  FC_REQUIRE(workspace && aligned(workspace, 256), FC_EINVAL, "workspace must be non-null and 256-byte aligned");
+  FC_REQUIRE(ws_bytes >= need, FC_EINVAL, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  return cuda_status(fc::launch_group_norm_bwd(dy, x, weight, bias, gate, dx, dweight, dbias, dgate, B, L, C, G, eps,
+                                               channel_major, norm_vec(L, C, G, channel_major, e), (float*)workspace,
+                                               dtype, (cudaStream_t)stream),
+                     "group_norm_act_bwd launch");
+}
+
 }  // extern "C"

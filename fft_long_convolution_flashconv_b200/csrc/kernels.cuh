@@ -5,6 +5,7 @@
 #include <stddef.h>
 
 #include "common.cuh"
+#include "scan.cuh"
 
 namespace fc {
 
@@ -112,5 +113,39 @@ cudaError_t launch_fftconv_long(const void* u, const float* f, const float* D, v
                                 void* workspace, int dtype, cudaStream_t st);
 // Tensor-core filter generation CTAs that gave up waiting for an MMA.
 unsigned int gen_tc_timeouts();
+
+// Short causal convolution by channels (short_conv.cu); rows.cuh has Rows.
+// out_vec: output rows start on 16-byte boundaries.  part: float scratch of
+// short_conv_bwd_splits() * H * (K + 1).
+cudaError_t launch_short_conv(const Rows& x, const float* w, const float* bias, void* y, int B, int H, int L, int K,
+                              int silu, const int* lengths, const void* state_in, void* state_out, int out_vec,
+                              int dtype, cudaStream_t st);
+int short_conv_bwd_splits(int B, int H, int L);
+cudaError_t launch_short_conv_bwd(const Rows& dy, const Rows& x, const float* w, const float* bias, void* dx, float* dw,
+                                  float* dbias, int B, int H, int L, int K, int silu, const int* lengths,
+                                  const void* state_in, const void* dstate_out, void* dstate_in, float* part,
+                                  int out_vec, int dtype, cudaStream_t st);
+cudaError_t launch_short_conv_step(const void* x, long long xs, void* state, const float* w, const float* bias, void* y,
+                                   int B, int H, int K, int silu, const int* slots, int S, int dtype, cudaStream_t st);
+
+// Selective scan (selective_scan.cu, selective_scan_bwd.cu); scan.cuh has
+// ScanArgs.  ckpt: B x H x ceil(L / 64) x N states entering the 64-step blocks.
+cudaError_t launch_selective_scan(const ScanArgs& p, void* y, float* state_out, float* ckpt, int dtype,
+                                  cudaStream_t st);
+cudaError_t launch_selective_scan_step(const ScanArgs& p, float* state, void* y, const int* slots, int S, int dtype,
+                                       cudaStream_t st);
+size_t selective_scan_bwd_workspace_bytes(int B, int H, int L, int N, int G);
+cudaError_t launch_selective_scan_bwd(const ScanArgs& p, const float* ckpt, void* du, void* ddelta, float* dA, void* dB,
+                                      void* dC, float* dD, float* ddt_bias, void* dz, const float* dstate_out,
+                                      float* dstate_in, void* workspace, int dtype, cudaStream_t st);
+
+// Group norm of each token with SiLU (group_norm.cu).  vec: rows and groups
+// start on 16-byte boundaries.  part: float scratch of group_norm_bwd_splits() * 2 C.
+cudaError_t launch_group_norm(const void* x, const float* w, const float* bias, const void* gate, void* y, int B, int L,
+                              int C, int G, float eps, int channel_major, int vec, int dtype, cudaStream_t st);
+int group_norm_bwd_splits(int B, int L, int C, int G, int channel_major);
+cudaError_t launch_group_norm_bwd(const void* dy, const void* x, const float* w, const float* bias, const void* gate,
+                                  void* dx, float* dw, float* dbias, void* dgate, int B, int L, int C, int G, float eps,
+                                  int channel_major, int vec, float* part, int dtype, cudaStream_t st);
 
 }  // namespace fc

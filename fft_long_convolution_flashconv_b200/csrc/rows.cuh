@@ -1,0 +1,143 @@
+// Rows of a sequence tensor for the selective-SSM kernels: eight time steps
+// per thread, loaded and stored as 16-byte vectors where a row allows it.
+#pragma once
+
+#include <limits.h>
+
+#include "common.cuh"
+
+namespace fc {
+
+constexpr int kVec = 8;  // time steps per thread and load
+
+// A B x H x L (or B x G x N x L) tensor with contiguous time: element strides of
+// a batch, of a row and of a group; vec = every row starts on a 16-byte boundary.
+struct Rows {
+  const void* p;
+  long long bs, rs, gs;
+  int vec;
+};
+
+template <typename T> struct Raw8;  // eight elements as loaded
+template <> struct Raw8<float> { float4 a, b; };
+template <> struct Raw8<__half> { uint4 a; };
+template <> struct Raw8<__nv_bfloat16> { uint4 a; };
+
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
+  v[0] = r.a.x; v[1] = r.a.y; v[2] = r.a.z; v[3] = r.a.w;
+  v[4] = r.b.x; v[5] = r.b.y; v[6] = r.b.z; v[7] = r.b.w;
+}
+__device__ __forceinline__ void unpack8(const Raw8<__half>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+    v[2 * i] = f.x;
+    v[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw8<__nv_bfloat16>& r, float (&v)[8]) {
+  const uint32_t w[4] = {r.a.x, r.a.y, r.a.z, r.a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {  // a bfloat16 is the upper half of a float
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ void ldraw8(const float* p, Raw8<float>& r) {
+  r.a = __ldg(reinterpret_cast<const float4*>(p));
+  r.b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+}
+template <typename T>
+__device__ __forceinline__ void ldraw8(const T* p, Raw8<T>& r) {
+  r.a = __ldg(reinterpret_cast<const uint4*>(p));
+}
+
+// Elements t0 .. t0 + 7 of a row of length L as floats; those at n and behind
+// it (n <= L) are zero whatever memory holds there.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, long long t0, int L, int n, bool vec, float (&v)[8]) {
+  if (vec && t0 + 8 <= L) {
+    Raw8<T> r;
+    ldraw8(row + t0, r);
+    unpack8(r, v);
+    if (t0 + 8 > n) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (t0 + i >= n) v[i] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = t0 + i < n ? IO<T>::ld(row + t0 + i) : 0.f;
+  }
+}
+
+__device__ __forceinline__ void stvec8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void stvec8(__half* p, const float (&v)[8]) {
+  uint4 o;
+  uint32_t* w = &o.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = o;
+}
+__device__ __forceinline__ void stvec8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint4 o;
+  uint32_t* w = &o.x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&h);
+  }
+  *reinterpret_cast<uint4*>(p) = o;
+}
+
+// Store v at t0 .. t0 + 7 of an output row of length L (zeros at n and behind).
+template <typename T>
+__device__ __forceinline__ void store8(T* row, long long t0, int L, int n, bool vec, float (&v)[8]) {
+  if (t0 + 8 > n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t0 + i >= n) v[i] = 0.f;
+  }
+  if (vec && t0 + 8 <= L) {
+    stvec8(row + t0, v);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t0 + i < L) IO<T>::st(row + t0 + i, v[i]);
+  }
+}
+
+// lengths[b] clamped to [0, L]; L without lengths.
+__device__ __forceinline__ int row_length(const int* lengths, int b, int L) {
+  return lengths ? min(max(__ldg(lengths + b), 0), L) : L;
+}
+
+// Sigmoid and SiLU x s(x).  exp(-x) = infinity for x < -88 gives s = 0.
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+__device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
+// Derivative of SiLU.
+__device__ __forceinline__ float dsilu(float x) {
+  const float s = sigmoid(x);
+  return s * fmaf(x, 1.f - s, 1.f);
+}
+
+// Row b of a decode batch: its place in the state pool, or -1 for a padded row
+// (a slot outside [0, S), or one that an earlier row of the batch holds).
+// Every thread of the block calls it.
+__device__ __forceinline__ int batch_slot(const int* slots, int b, int S) {
+  if (!slots) return b;
+  const int slot = __ldg(slots + b);
+  bool taken = slot < 0 || slot >= S;
+  for (int i = threadIdx.x; i < b; i += blockDim.x) taken |= __ldg(slots + i) == slot;
+  return __syncthreads_or(taken) ? -1 : slot;
+}
+
+}  // namespace fc

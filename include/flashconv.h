@@ -302,6 +302,131 @@ FC_API fc_status h3_mixer_decode_step(const void* q, const void* k, const void* 
                                       const float* Cp, const float* D, void* o, int B, int heads, int head_dim,
                                       int N, int shift_len, long long pos, fc_dtype dtype, void* stream);
 
+/* ---- The selective SSM: input-dependent step size, input and output vectors --
+ * Sequences, strides and padded batches of the calls below:
+ *  - x, u, delta, z, dy are B x H x L; Bt and Ct are B x G x N x L (channel h
+ *    reads group h / (H / G)).  Time is contiguous; the other strides, in
+ *    elements, come in `strides` (a host array, read during the call: the
+ *    entries that each call names, batch first), NULL when every input is
+ *    contiguous.  Inputs are aligned to their elements; rows on 16-byte
+ *    boundaries run faster.  Outputs are contiguous and 16-byte aligned where
+ *    they are sequences; no output overlaps an input or another output.
+ *  - lengths: B int32 on the device, or NULL (every row has L steps).  A value
+ *    outside [0, L] counts as the nearer end.  Outputs and gradients at t >=
+ *    lengths[b] are zeros, inputs there are never used (whatever they hold),
+ *    and a state is the one after the row's last step.
+ *  - slots (single tokens): B int32 on the device, the rows of a state pool
+ *    with S rows; NULL: row b uses state b, and S == B.  A slot outside [0, S)
+ *    or one that an earlier row of the batch holds marks a padded row: its y is
+ *    zero and it reads and writes no state.  B <= 65535.
+ *  - A workspace serves one call at a time: calls that may overlap on the GPU
+ *    (other streams, graphs replayed side by side) need one each.
+ *  - Results do not depend on the order in which blocks run: the same call
+ *    gives the same bits.
+ * Limits: 1 <= L <= 2^30, B * H * ceil(L / 1024) < 2^31, N <= 256, K <= 8. */
+
+/* short_conv_fwd -- short causal convolution by channels with bias and SiLU,
+ * the layer in front of a selective scan (the mixer's shift SSM on its own).
+ *   c[t] = bias[h] + sum_{j<K} w[h,j] x[t-j]     (tap 0 = the current token)
+ *   y[t] = silu != 0 ? c / (1 + exp(-c)) : c
+ * w: H x K floats; bias: H floats or NULL; state_in: B x H x (K-1) in `dtype`,
+ * the inputs at times -(K-1) .. -1, or NULL (zeros); state_out: the same of the
+ * row's last K-1 inputs, or NULL.  strides: x batch, row.
+ * Precision: float32 arithmetic, y rounded once. */
+FC_API fc_status short_conv_fwd(const void* x, const float* w, const float* bias, void* y, int B, int H, int L, int K,
+                                int silu, const int* lengths, const long long* strides, const void* state_in,
+                                void* state_out, fc_dtype dtype, void* stream);
+
+/* short_conv_bwd -- gradients of short_conv_fwd given dy and, or NULL,
+ * dstate_out (of state_out): with dc = dy silu'(c),
+ *   dx[s] = sum_j w[j] dc[s+j] (+ dstate_out),  dw[j] = sum_{b,t} dc[t] x[t-j],
+ *   dbias = sum dc;  dstate_in likewise (NULL: not written).
+ * dw: H x K; dbias: H or NULL.  strides: dy batch, row, x batch, row.
+ * workspace: short_conv_bwd_workspace(...) bytes, 256-byte aligned.
+ * Precision: float32 arithmetic and sums. */
+FC_API size_t short_conv_bwd_workspace(int B, int H, int L, int K);
+FC_API fc_status short_conv_bwd(const void* dy, const void* x, const float* w, const float* bias, void* dx, float* dw,
+                                float* dbias, int B, int H, int L, int K, int silu, const int* lengths,
+                                const long long* strides, const void* state_in, const void* dstate_out,
+                                void* dstate_in, void* workspace, size_t ws_bytes, fc_dtype dtype, void* stream);
+
+/* short_conv_step -- one token: x, y: B x H (x with batch stride x_stride);
+ * state: S x H x (K-1) in `dtype`, oldest first (short_conv_fwd's state_out),
+ * updated in place (NULL allowed when K == 1). */
+FC_API fc_status short_conv_step(const void* x, void* state, const float* w, const float* bias, void* y, int B, int H,
+                                 int K, int silu, const int* slots, int S, long long x_stride, fc_dtype dtype,
+                                 void* stream);
+
+/* selective_scan_fwd -- the diagonal SSM with input-dependent dt, B and C:
+ *   dt = softplus(delta + dt_bias)  (delta + dt_bias itself where softplus == 0)
+ *   x_n <- exp(dt A[h,n]) x_n + dt B_n u,   y = sum_n C_n x_n + D u,  times z / (1 + exp(-z)) with a gate
+ * (the recurrent view of ssm_decode_step with a real A and parameters that
+ * change from step to step, so no convolution filter exists).
+ * A: H x N floats; D, dt_bias: H floats or NULL; z: gate or NULL; state_in,
+ * state_out: B x H x N floats or NULL.  ckpt: selective_scan_ckpt_bytes(...)
+ * bytes for selective_scan_bwd (the states entering the 64-step blocks), or
+ * NULL.  strides: batch, row of u, delta, z; batch, group, row of Bt, Ct (12).
+ * Precision: float32 state and arithmetic (exponentials by the special
+ * function unit, relative error about 2^-22), y rounded once. */
+FC_API size_t selective_scan_ckpt_bytes(int B, int H, int L, int N);
+FC_API fc_status selective_scan_fwd(const void* u, const void* delta, const float* A, const void* Bt, const void* Ct,
+                                    const float* D, const float* dt_bias, const void* z, void* y, int B, int H, int L,
+                                    int N, int G, int softplus, const int* lengths, const long long* strides,
+                                    const float* state_in, float* state_out, float* ckpt, fc_dtype dtype,
+                                    void* stream);
+
+/* selective_scan_bwd -- gradients of selective_scan_fwd given dy, the same
+ * inputs, the ckpt that it wrote and, or NULL, dstate_out (of state_out).
+ * With dyp = dy silu(z) and g_n[t] = C_n dyp + a_n[t+1] g_n[t+1], a = exp(dt A):
+ *   du = D dyp + dt sum_n g_n B_n;  ddt = u sum_n g_n B_n + sum_n A_n g_n a_n x_n[t-1]
+ *   ddelta = ddt softplus'(delta + dt_bias);  dz = dy y silu'(z)
+ *   dA = sum_{b,t} dt g a x[t-1];  dD = sum dyp u;  ddt_bias = sum ddelta
+ *   dB_n = sum_h g_n dt u,  dC_n = sum_h dyp x_n  over the group's channels
+ * du, ddelta, dz: B x H x L, dB, dC: B x G x N x L in `dtype`; dA: H x N
+ * floats; dD, ddt_bias: H floats or NULL; dz given where z is; dstate_in: B x
+ * H x N floats or NULL.  strides: dy batch, row, then as selective_scan_fwd
+ * (14).  workspace: selective_scan_bwd_workspace(...) bytes, 256-byte aligned.
+ * Precision: float32 states, sums and arithmetic. */
+FC_API size_t selective_scan_bwd_workspace(int B, int H, int L, int N, int G);
+FC_API fc_status selective_scan_bwd(const void* dy, const void* u, const void* delta, const float* A, const void* Bt,
+                                    const void* Ct, const float* D, const float* dt_bias, const void* z,
+                                    const float* ckpt, void* du, void* ddelta, float* dA, void* dB, void* dC, float* dD,
+                                    float* ddt_bias, void* dz, int B, int H, int L, int N, int G, int softplus,
+                                    const int* lengths, const long long* strides, const float* dstate_out,
+                                    float* dstate_in, void* workspace, size_t ws_bytes, fc_dtype dtype, void* stream);
+
+/* selective_scan_step -- one token: u, delta, z, y: B x H, Bt, Ct: B x G x N;
+ * state: S x H x N floats, updated in place (selective_scan_fwd's state_out).
+ * strides: as selective_scan_fwd, the row stride being that of a channel (u,
+ * delta, z) or of a state (Bt, Ct); NULL when contiguous. */
+FC_API fc_status selective_scan_step(const void* u, const void* delta, const float* A, const void* Bt, const void* Ct,
+                                     const float* D, const float* dt_bias, const void* z, float* state, void* y, int B,
+                                     int H, int N, int G, int softplus, const int* slots, int S,
+                                     const long long* strides, fc_dtype dtype, void* stream);
+
+/* group_norm_act_fwd -- group norm of every token on its own (a causal model
+ * stays causal) with SiLU, for a mixer's output, one group a head:
+ *   n = (x - mean) / sqrt(var + eps) weight + bias over the C / G channels of a
+ *   group of one token;  y = silu(n), or n silu(gate) with a gate
+ * x, gate: B x L x C (h3_mixer_fwd's output), or with channel_major B x C x L
+ * (selective_scan_fwd's output); y: B x L x C; weight, bias: C floats or NULL
+ * (1, 0).  All contiguous and 16-byte aligned.  Limits: C / G <= 8192, G <=
+ * 65535, B * L * G < 2^31, eps > 0.  Precision: float32 (mean first, then the
+ * squares around it), y rounded once. */
+FC_API fc_status group_norm_act_fwd(const void* x, const float* weight, const float* bias, const void* gate, void* y,
+                                    int B, int L, int C, int G, float eps, int channel_major, fc_dtype dtype,
+                                    void* stream);
+
+/* group_norm_act_bwd -- gradients of group_norm_act_fwd given dy (B x L x C):
+ * dx and dgate in x's layout (dgate given where gate is); dweight, dbias: C
+ * floats, each or NULL.  workspace: group_norm_act_bwd_workspace(...) bytes,
+ * 256-byte aligned. */
+FC_API size_t group_norm_act_bwd_workspace(int B, int L, int C, int G, int channel_major);
+FC_API fc_status group_norm_act_bwd(const void* dy, const void* x, const float* weight, const float* bias,
+                                    const void* gate, void* dx, float* dweight, float* dbias, void* dgate, int B, int L,
+                                    int C, int G, float eps, int channel_major, void* workspace, size_t ws_bytes,
+                                    fc_dtype dtype, void* stream);
+
 /* ssm_conv_fwd_noalloc -- ssm_conv_fwd for callers that cannot allocate
  * device memory.  The pages have no counterpart to this call.
  *
