@@ -51,7 +51,8 @@ SIGNATURES = {
     "short_conv_step": (_i, [_vp, _vp, _fp, _fp, _vp, _i, _i, _i, _i, _vp, _i, ctypes.c_longlong, _i, _vp]),
     "selective_scan_ckpt_bytes": (_sz, [_i, _i, _i, _i]),
     "selective_scan_fwd": (_i, [_vp, _vp, _fp, _vp, _vp, _fp, _fp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _fp,
-                                _fp, _fp, _i, _vp]),
+                                _fp, _fp, _vp, _sz, _i, _vp]),
+    "selective_scan_workspace": (_sz, [_i, _i, _i, _i, _i]),
     "selective_scan_bwd_workspace": (_sz, [_i, _i, _i, _i, _i]),
     "selective_scan_bwd": (_i, [_vp, _vp, _vp, _fp, _vp, _vp, _fp, _fp, _vp, _fp, _vp, _vp, _fp, _vp, _vp, _fp, _fp,
                                 _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _fp, _fp, _vp, _sz, _i, _vp]),

@@ -481,7 +481,8 @@ def selective_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bt
                        D: Optional[torch.Tensor] = None, dt_bias: Optional[torch.Tensor] = None,
                        z: Optional[torch.Tensor] = None, softplus: bool = True,
                        state_in: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
-                       return_state: bool = False, return_ckpt: bool = False, out: Optional[torch.Tensor] = None):
+                       return_state: bool = False, return_ckpt: bool = False,
+                       workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None):
     """Selective scan: dt = softplus(delta + dt_bias), x <- exp(dt A) x + dt B u,
     y = (C x + D u) silu(z); u, delta, z: B x H x L, A: H x N, Bt, Ct: B x G x N x L.
     Returns y, then the final state (B x H x N float32) if return_state, then what
@@ -500,13 +501,21 @@ def selective_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bt
     ckpt = None
     if return_ckpt:
         ckpt = torch.empty(int(lib.selective_scan_ckpt_bytes(B, H, L, N)) // 4, dtype=torch.float32, device=dev)
+    need = int(lib.selective_scan_workspace(B, H, L, N, G))
+    if need or workspace is not None:
+        workspace = _need(workspace, need, dev)
     with _Call(dev) as st:
         check(lib.selective_scan_fwd(_addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D), _addr(dt_bias),
                                      _addr(z), _addr(out), B, H, L, N, G, bool(softplus), _addr(lengths),
-                                     _strides(*strides), _addr(state_in), _addr(state), _addr(ckpt), _DT[u.dtype], st),
-              "selective_scan_fwd")
+                                     _strides(*strides), _addr(state_in), _addr(state), _addr(ckpt), _addr(workspace),
+                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                     _DT[u.dtype], st), "selective_scan_fwd")
     more = ((state,) if return_state else ()) + ((ckpt,) if return_ckpt else ())
     return (out, *more) if more else out
+
+
+def selective_scan_workspace_bytes(B: int, H: int, L: int, N: int, G: int) -> int:
+    return int(_lib.load().selective_scan_workspace(B, H, L, N, G))
 
 
 def selective_scan_bwd_workspace_bytes(B: int, H: int, L: int, N: int, G: int) -> int:

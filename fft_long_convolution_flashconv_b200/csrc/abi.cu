@@ -664,11 +664,16 @@ FC_API size_t selective_scan_ckpt_bytes(int B, int H, int L, int N) {
   return (size_t)B * H * (((size_t)L + fc::kCkptSteps - 1) / fc::kCkptSteps) * N * 4;
 }
 
+FC_API size_t selective_scan_workspace(int B, int H, int L, int N, int G) {
+  if (B < 1 || H < 1 || L < 1 || N < 1 || G < 1 || H % G) return 0;
+  return fc::selective_scan_workspace_bytes(B, H, L, N, G);
+}
+
 FC_API fc_status selective_scan_fwd(const void* u, const void* delta, const float* A, const void* Bt, const void* Ct,
                                     const float* D, const float* dt_bias, const void* z, void* y, int B, int H, int L,
                                     int N, int G, int softplus, const int* lengths, const long long* strides,
-                                    const float* state_in, float* state_out, float* ckpt, fc_dtype dtype,
-                                    void* stream) {
+                                    const float* state_in, float* state_out, float* ckpt, void* workspace,
+                                    size_t ws_bytes, fc_dtype dtype, void* stream) {
   g_err[0] = 0;
   fc::ScanArgs p;
   fc_status s = scan_args(&p, u, delta, A, Bt, Ct, D, dt_bias, z, B, H, L, N, G, softplus, lengths, strides, dtype);
@@ -686,7 +691,12 @@ FC_API fc_status selective_scan_fwd(const void* u, const void* delta, const floa
   FC_REQUIRE(!hits_scan_input(p, e, ckpt, ce) && !overlap(y, ye, ckpt, ce) && !overlap(state_in, se, ckpt, ce) &&
                  !overlap(state_out, se, ckpt, ce),
              FC_EINVAL, "ckpt overlaps another array");
-  return cuda_status(fc::launch_selective_scan(p, y, state_out, ckpt, dtype, (cudaStream_t)stream),
+  const size_t need = selective_scan_workspace(B, H, L, N, G);
+  if (need) {
+    FC_REQUIRE(workspace && aligned(workspace, 256), FC_EINVAL, "workspace must be non-null and 256-byte aligned");
+    FC_REQUIRE(ws_bytes >= need, FC_EINVAL, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  }
+  return cuda_status(fc::launch_selective_scan(p, y, state_out, ckpt, workspace, dtype, (cudaStream_t)stream),
                      "selective_scan_fwd launch");
 }
 

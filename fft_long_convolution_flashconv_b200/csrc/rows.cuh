@@ -54,13 +54,40 @@ __device__ __forceinline__ void ldraw8(const T* p, Raw8<T>& r) {
   r.a = __ldg(reinterpret_cast<const uint4*>(p));
 }
 
+// The eight elements from p on, p not on a 16-byte boundary: the two aligned
+// vectors around them, moved down by p's offset in the first.  Both vectors have
+// to lie in the row (see inner8).
+template <typename T>
+__device__ __forceinline__ void ldraw8_any(const T* p, Raw8<T>& r) {
+  static_assert(sizeof(T) == 2, "two 16-byte vectors hold eight 16-bit elements at any offset");
+  const uintptr_t m = reinterpret_cast<uintptr_t>(p) & 15;
+  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - m);
+  const uint4 a = __ldg(q), b = __ldg(q + 1);
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 6; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
+#pragma unroll
+  for (int i = 0; i < 5; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
+  const uint32_t sh = (uint32_t)(m & 2) * 8;
+  r.a = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh), __funnelshift_r(w[2], w[3], sh),
+                   __funnelshift_r(w[3], w[4], sh));
+}
+__device__ __forceinline__ bool inner8(long long t0, int L) { return t0 >= 8 && t0 + 16 <= L; }
+
 // Elements t0 .. t0 + 7 of a row of length L as floats; those at n and behind
 // it (n <= L) are zero whatever memory holds there.
 template <typename T>
 __device__ __forceinline__ void load8(const T* row, long long t0, int L, int n, bool vec, float (&v)[8]) {
-  if (vec && t0 + 8 <= L) {
+  if (vec ? t0 + 8 <= L : sizeof(T) == 2 && inner8(t0, L)) {
     Raw8<T> r;
-    ldraw8(row + t0, r);
+    if constexpr (sizeof(T) == 2) {
+      if (vec)
+        ldraw8(row + t0, r);
+      else
+        ldraw8_any(row + t0, r);
+    } else {
+      ldraw8(row + t0, r);
+    }
     unpack8(r, v);
     if (t0 + 8 > n) {
 #pragma unroll

@@ -4,14 +4,13 @@
 //   dt = softplus(delta + dt_bias),  a_n = exp(dt A_n)
 //   x_n <- a_n x_n + dt B_n u,  y = (sum_n C_n x_n + D u) silu(z)
 //
-// A lane holds eight steps of one channel in registers and runs through the
-// states one after the other: it forms a_n and dt B_n u for its steps, runs
-// the recurrence from zero, joins the lanes of a channel by a scan of (product
-// of a, end state) over shuffles, runs the recurrence again from the state
-// that enters it and adds C_n x_n to its eight outputs.  The product of a over
-// a lane is exp(A_n sum dt), one exponential.  TL lanes are a channel's
-// TL * 8 steps, so global rows are read in 16-byte vectors of neighbouring
-// lanes; a block's channels share B and C through shared memory.
+// A lane holds sixteen steps of one channel in registers and runs through the
+// states: it forms a_n and dt B_n u for its steps, runs the recurrence from
+// zero, joins the four lanes of a channel by a scan of (product of a, end
+// state) over shuffles, runs the recurrence again from the state that enters it
+// and adds C_n x_n to its outputs.  The product of a over a lane is
+// exp(A_n sum dt), one exponential.  Four lanes of sixteen steps are a 64-step
+// block; a warp takes eight channels.
 #include "kernels.cuh"
 #include "scan.cuh"
 
@@ -21,132 +20,416 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStates = 16;  // states whose B and C are in shared memory at a time
+constexpr int TB = kCkptSteps;
+constexpr int kMinBlocks = 4;  // resident on an SM
+// A lane's steps, and what follows: the lanes of a channel, the channels of a warp and of a block.
+template <int TPL_>
+struct Shape {
+  static constexpr int TPL = TPL_, PAIRS = TPL / 2, VPL = TPL / kVec, TL = TB / TPL, CL = 32 / TL, CH = kWarps * CL;
+  // States in flight in a lane, groups of them in one schedule: four states' work fills the 128 registers that four
+  // blocks an SM leave (eight steps: 172 us; two states: 177; sixteen steps: 291; with 168 registers and two states 352).
+  static constexpr int SG = TPL == 8 ? 4 : 1, kUnroll = TPL == 8 ? 1 : 4;
+};
 
-template <typename T, int TL>
-__global__ __launch_bounds__(kThreads) void scan_kernel(ScanArgs p, T* y, float* state_out, float* ckpt, int tiles) {
-  constexpr int CL = 32 / TL, TB = TL * 8, CH = kWarps * CL;
+__device__ __forceinline__ uint32_t shared_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// Eight steps of a row on their way into 8 sizeof(T) bytes of shared memory of
+// the calling thread's own: asynchronous copies where the row's alignment allows
+// them, else through registers (what is at n and behind may come along or not;
+// take8 drops it).
+template <typename T>
+__device__ __forceinline__ void fetch8(T* slot, const T* row, long long t0, int L, int n, bool vec) {
+  if (vec && t0 + 8 <= L) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared_addr(slot) + 16 * i),
+                   "l"((const char*)(row + t0) + 16 * i));
+    return;
+  }
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t0 + i < n)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_addr(slot + i)), "l"(row + t0 + i));
+      else
+        slot[i] = T(0.f);
+  } else if (inner8(t0, L)) {
+    ldraw8_any(row + t0, *reinterpret_cast<Raw8<T>*>(slot));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) slot[i] = t0 + i < n ? row[t0 + i] : T(0.f);
+  }
+}
+__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// The slot's steps as floats, zeros at n and behind.
+template <typename T>
+__device__ __forceinline__ void take8(const T* slot, long long t0, int n, float (&v)[8]) {
+  Raw8<T> r = *reinterpret_cast<const Raw8<T>*>(slot);
+  unpack8(r, v);
+  if (t0 + 8 > n) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (t0 + i >= n) v[i] = 0.f;
+  }
+}
+
+// Place of step t of a block in a row of the B / C tiles: the first four steps
+// of every lane, then the next four and so on, so that the 16-byte reads of a
+// warp's lanes are contiguous.
+template <int TPL>
+__device__ __forceinline__ int tile_at(int t) {
+  return (t % TPL / 4) * (TB / TPL * 4) + t / TPL * 4 + t % 4;
+}
+
+// B and C of up to kStates states of a block: raw vectors into the thread's
+// slots, then as floats into the tile that the block computes from.
+template <typename T, int TPL>
+struct Tiles {
+  static constexpr int kRow = TB / 8, kPer = kStates * kRow / kThreads;  // vectors of a row, of a thread (B, and C)
+  const T *Bt, *Ct;
+  T* slot;  // 2 kPer * 8 elements
+  __device__ __forceinline__ void fetch(const ScanArgs& p, int s0, int ns, int tb, int n) const {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = threadIdx.x + j * kThreads, s = i / kRow, t0 = tb + i % kRow * 8;
+      if (s < ns) {
+        fetch8(slot + j * 8, Bt + (s0 + s) * p.Bt.rs, t0, p.L, n, p.Bt.vec);
+        fetch8(slot + (kPer + j) * 8, Ct + (s0 + s) * p.Ct.rs, t0, p.L, n, p.Ct.vec);
+      }
+    }
+  }
+  // Rows from ns on, which fill up a group of states, are zeros.
+  __device__ __forceinline__ void store(float* buf, int ns, int tb, int n) const {
+#pragma unroll
+    for (int j = 0; j < 2 * kPer; ++j) {
+      const int i = threadIdx.x + j % kPer * kThreads, s = i / kRow, k = i % kRow;
+      float v[8] = {};
+      if (s < ns) take8(slot + j * 8, tb + k * 8, n, v);
+      float* d = buf + (j / kPer * kStates + s) * TB;
+      *reinterpret_cast<float4*>(d + tile_at<TPL>(k * 8)) = make_float4(v[0], v[1], v[2], v[3]);
+      *reinterpret_cast<float4*>(d + tile_at<TPL>(k * 8 + 4)) = make_float4(v[4], v[5], v[6], v[7]);
+    }
+  }
+};
+
+// The two words below are read again only behind a block barrier, so the
+// compiler is told of no memory: the next states' loads may pass the store.
+__device__ __forceinline__ void put_shared(uint32_t at, float v) {
+  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v));
+}
+__device__ __forceinline__ void put_global(bool on, float* p, float v) {
+  asm volatile("{ .reg .pred q; setp.ne.s32 q, %0, 0; @q st.global.f32 [%1], %2; }" ::"r"((int)on), "l"(p), "f"(v));
+}
+
+// Step D of the scan over a channel's lanes: lane t joins what lane t - D
+// holds, h = P h' + h and P = P P' (not after the last step); lanes below D keep
+// theirs.  One predicated instruction each instead of a branch keeps several
+// states' work in one schedule.
+template <int TL, int D>
+__device__ __forceinline__ void join(float& h, float& P) {
+  constexpr int kClamp = (32 - TL) << 8;
+  if (D * 2 < TL)
+    asm volatile(
+        "{ .reg .pred q; .reg .f32 t, s; shfl.sync.up.b32 t|q, %0, %2, %3, -1; shfl.sync.up.b32 s, %1, %2, %3, -1;\n"
+        "@q fma.rn.f32 %0, %1, t, %0; @q mul.rn.f32 %1, %1, s; }"
+        : "+f"(h), "+f"(P)
+        : "n"(D), "n"(kClamp));
+  else
+    asm volatile("{ .reg .pred q; .reg .f32 t; shfl.sync.up.b32 t|q, %0, %2, %3, -1; @q fma.rn.f32 %0, %1, t, %0; }"
+                 : "+f"(h)
+                 : "f"(P), "n"(D), "n"(kClamp));
+}
+// h of the lane before; the first lane of a channel keeps `first`.
+template <int TL>
+__device__ __forceinline__ float before(float h, float first) {
+  asm volatile("{ .reg .pred q; .reg .f32 t; shfl.sync.up.b32 t|q, %1, 1, %2, -1; @q mov.f32 %0, t; }"
+               : "+f"(first)
+               : "f"(h), "n"((32 - TL) << 8));
+  return first;
+}
+
+// The steps of a lane: step sizes, dt u and the outputs so far.
+template <int PAIRS>
+struct Lane {
+  float2 dt[PAIRS], du[PAIRS], o[PAIRS];
+  float sum;  // of dt
+};
+
+// SG states of a block, rows from Bs on, for a lane's steps: o += C x.  As: the
+// states' A log2(e), rows of CH channels; x0s: the state entering the first lane
+// of a channel, zeros for the others; x1s: where the last lane's end state goes
+// (the others write to a place that nothing reads).  OUT: outputs are wanted,
+// not only states.
+template <typename S, bool OUT, bool CKPT>
+__device__ __forceinline__ void run_states(const float* Bs, const float* As, const float* x0s, uint32_t x1s, int tl,
+                                           Lane<S::PAIRS>& l, bool keep, float* ckpt, int nlive) {
+  constexpr int SG = S::SG, PAIRS = S::PAIRS, TPL = S::TPL, TL = S::TL, CH = S::CH;
+  float2 a[SG][PAIRS], w[SG][PAIRS];
+  float h[SG], P[SG], x0[SG];
+#pragma unroll
+  for (int q = 0; q < SG; ++q) {
+    const float4* Bp = reinterpret_cast<const float4*>(Bs + q * TB) + tl;
+    const float A2 = As[q * CH];
+    x0[q] = x0s[q * CH];
+#pragma unroll
+    for (int i = 0; i < TPL / 4; ++i) {
+      const float4 v = Bp[i * TL];
+      w[q][2 * i] = mul2(l.du[2 * i], make_float2(v.x, v.y));
+      w[q][2 * i + 1] = mul2(l.du[2 * i + 1], make_float2(v.z, v.w));
+    }
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+      const float2 e = mul2(l.dt[i], both(A2));
+      a[q][i] = make_float2(ex2(e.x), ex2(e.y));
+    }
+    P[q] = ex2(l.sum * A2);
+  }
+#pragma unroll
+  for (int q = 0; q < SG; ++q) {
+    float v = fmaf(a[q][0].y, w[q][0].x, w[q][0].y);
+#pragma unroll
+    for (int i = 1; i < PAIRS; ++i) {
+      v = fmaf(a[q][i].x, v, w[q][i].x);
+      v = fmaf(a[q][i].y, v, w[q][i].y);
+    }
+    h[q] = fmaf(P[q], x0[q], v);
+  }
+  // states at the end of every lane
+#pragma unroll
+  for (int q = 0; q < SG; ++q) join<TL, 1>(h[q], P[q]);
+#pragma unroll
+  for (int q = 0; q < SG; ++q) join<TL, 2>(h[q], P[q]);
+  if constexpr (TL > 4) {
+#pragma unroll
+    for (int q = 0; q < SG; ++q) join<TL, 4>(h[q], P[q]);
+  }
+#pragma unroll
+  for (int q = 0; q < SG; ++q) {
+    put_shared(x1s + q * CH * 4, h[q]);
+    if (!OUT) continue;
+    const float4* Cp = reinterpret_cast<const float4*>(Bs + (kStates + q) * TB) + tl;
+    float v = before<TL>(h[q], x0[q]);
+    if (CKPT) put_global(keep && q < nlive, ckpt + q, v);
+#pragma unroll
+    for (int i = 0; i < TPL / 4; ++i) {
+      const float4 cv = Cp[i * TL];
+      float2 x, z;
+      x.x = v = fmaf(a[q][2 * i].x, v, w[q][2 * i].x);
+      x.y = v = fmaf(a[q][2 * i].y, v, w[q][2 * i].y);
+      z.x = v = fmaf(a[q][2 * i + 1].x, v, w[q][2 * i + 1].x);
+      z.y = v = fmaf(a[q][2 * i + 1].y, v, w[q][2 * i + 1].y);
+      l.o[2 * i] = fma2(make_float2(cv.x, cv.y), x, l.o[2 * i]);
+      l.o[2 * i + 1] = fma2(make_float2(cv.z, cv.w), z, l.o[2 * i + 1]);
+    }
+  }
+}
+
+// Shared memory of a scan block, in floats from the start.
+template <typename T, int TPL>
+struct Layout {
+  using S = Shape<TPL>;
+  static constexpr int VPL = S::VPL, CH = S::CH;
+  static constexpr int bc = 0;                  // [2][2 kStates][TB] B and C
+  static constexpr int raw = 4 * kStates * TB;  // [2 kPer][8] T of a thread: B and C on their way
+  static constexpr int in = raw + 2 * Tiles<T, TPL>::kPer * 8 * kThreads * (int)sizeof(T) / 4;  // [5][VPL] T vectors
+  static constexpr int states = in + 5 * VPL * 8 * kThreads * (int)sizeof(T) / 4;
+  // [4][Np][CH]: A log2(e); entering states; zeros; what nothing reads
+  static size_t bytes(int Np) { return (size_t)(states + 4 * Np * CH) * 4; }
+};
+
+// Long sequences of few channels are cut into segments of `seg` 64-step blocks,
+// so that the SMs fill: scan_kernel<kEnds> runs each segment but the last from a
+// zero state and keeps its end state and its sum of dt, join_segments_kernel turns
+// those into the states entering the segments, and the outputs follow segment by
+// segment.
+enum Mode { kOutputs, kOutputsCkpt, kEnds };
+
+struct Segments {
+  int tpl;            // steps of a lane: 8 or 16
+  int count, blocks;  // segments of a row; 64-step blocks of a segment
+  float* state;       // B x H x count x N (null: one segment)
+  float* dt;          // B x H x count
+};
+
+// A block of four warps takes CH channels of a group.
+template <typename T, int TPL, int MODE>
+__global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, Segments sg, T* y,
+                                                                                float* state_out, float* ckpt,
+                                                                                int tiles) {
+  using S = Shape<TPL>;
+  using Sm = Layout<T, TPL>;
+  constexpr int TL = S::TL, CL = S::CL, CH = S::CH, VPL = S::VPL, SG = S::SG;
+  constexpr bool OUT = MODE != kEnds, CKPT = MODE == kOutputsCkpt;
+  static_assert(kStates % SG == 0, "states come in whole groups");
   extern __shared__ float4 smem4[];
-  float* Bs = reinterpret_cast<float*>(smem4);  // [kStates][TB]
-  float* Cs = Bs + kStates * TB;
-  float* As = Cs + kStates * TB;  // [N][CH], A log2(e)
-  float* xs = As + p.N * CH;      // [N][CH], the state entering the block of steps
-  const int tid = threadIdx.x, lane = tid & 31, tl = lane % TL;
-  const int c = (tid >> 5) * CL + lane / TL;  // channel of the block
-  const int E = p.H / p.G;
-  const int tile = blockIdx.x % tiles, bg = blockIdx.x / tiles, b = bg / p.G, g = bg % p.G;
+  float* const sm = reinterpret_cast<float*>(smem4);
+  const int N = p.N, chunks = (N + kStates - 1) / kStates, Np = chunks * kStates;
+  float* const bc = sm + Sm::bc;
+  float* const As = sm + Sm::states;
+  float* const xs = As + Np * CH;
+  const int tid = threadIdx.x, lane = tid & 31, tl = lane % TL, c = (tid >> 5) * CL + lane / TL;
+  const int E = p.H / p.G, nseg = OUT ? sg.count : sg.count - 1;
+  const int seg = blockIdx.x % nseg, tile = blockIdx.x / nseg % tiles, bg = blockIdx.x / nseg / tiles;
+  const int b = bg / p.G, g = bg % p.G;
+  const int n = row_length(p.lengths, b, p.L);
+  for (int i = tid; i < Np * CH; i += kThreads) {
+    const int s = i / CH, cc = i % CH, hh = g * E + tile * CH + cc;
+    const bool ok = tile * CH + cc < E && s < N;
+    const long long row = (long long)b * p.H + hh;
+    As[i] = ok ? __ldg(p.A + (long long)hh * N + s) * kLog2e : 0.f;
+    xs[i] = !ok || !OUT ? 0.f
+            : sg.state  ? sg.state[(row * sg.count + seg) * N + s]
+            : p.state_in ? __ldg(p.state_in + row * N + s) : 0.f;
+    xs[Np * CH + i] = 0.f;
+  }
+  const float* const x0s = (tl == 0 ? xs : xs + Np * CH) + c;
+  const uint32_t x1s = shared_addr((tl == TL - 1 ? xs : xs + 2 * Np * CH) + c);
   const bool live = tile * CH + c < E;
   const int h = g * E + (live ? tile * CH + c : 0);
-  const long long row = (long long)b * p.H + h;
-  const int n = row_length(p.lengths, b, p.L);
-  const int N = p.N;
-  for (int i = tid; i < N * CH; i += kThreads) {
-    const int s = i / CH, cc = i % CH, hh = g * E + tile * CH + cc;
-    const bool ok = tile * CH + cc < E;
-    As[i] = ok ? __ldg(p.A + (long long)hh * N + s) * kLog2e : 0.f;
-    xs[i] = ok && p.state_in ? __ldg(p.state_in + ((long long)b * p.H + hh) * N + s) : 0.f;
-  }
+  const float Dh = p.D ? __ldg(p.D + h) : 0.f, bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
+  float total = 0.f;
   const T* u = (const T*)p.u.p + b * p.u.bs + h * p.u.rs;
   const T* delta = (const T*)p.delta.p + b * p.delta.bs + h * p.delta.rs;
   const T* z = p.z.p ? (const T*)p.z.p + b * p.z.bs + h * p.z.rs : nullptr;
-  const T* Bt = (const T*)p.Bt.p + b * p.Bt.bs + g * p.Bt.gs;
-  const T* Ct = (const T*)p.Ct.p + b * p.Ct.bs + g * p.Ct.gs;
-  const float Dh = p.D ? __ldg(p.D + h) : 0.f, bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
-  const int nck = (p.L + kCkptSteps - 1) / kCkptSteps;
-  for (int tb = 0; tb < p.L; tb += TB) {
-    const int t0 = tb + tl * 8;
-    float v[8], dt[8], du[8], o[8];
-    if (tb < n) {
-      load8(u, t0, p.L, n, p.u.vec, v);
-      load8(delta, t0, p.L, n, p.delta.vec, dt);
-      float sum = 0.f;
+  T* yr = y + ((long long)b * p.H + h) * p.L;
+  const Tiles<T, TPL> next{(const T*)p.Bt.p + b * p.Bt.bs + g * p.Bt.gs, (const T*)p.Ct.p + b * p.Ct.bs + g * p.Ct.gs,
+                      reinterpret_cast<T*>(sm + Sm::raw) + tid * 2 * Tiles<T, TPL>::kPer * 8};
+  T* const in = reinterpret_cast<T*>(sm + Sm::in) + tid * 8;
+  const int nck = (p.L + TB - 1) / TB;
+  const int first = seg * sg.blocks, last = min(nck, first + sg.blocks), end = min(last, (n + TB - 1) / TB);
+
+  Lane<S::PAIRS> l;
+  // u and delta of even and odd blocks, z
+  auto slot = [&](int which, int j) { return in + (which * VPL + j) * kThreads * 8; };
+  auto fetch = [&](int k) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float r = dt[i] + bias;
-        dt[i] = t0 + i < n ? (p.softplus ? softplus(r) : r) : 0.f;  // dt = 0 keeps the state
-        sum += dt[i];
-        du[i] = dt[i] * v[i];
-        o[i] = Dh * v[i];
-      }
-      for (int s0 = 0; s0 < N; s0 += kStates) {
-        const int ns = min(kStates, N - s0);
-        __syncthreads();
-        for (int i = tid; i < ns * TL; i += kThreads) {
-          const int s = i / TL, k = i % TL;
-          float w[8];
-          load8(Bt + (long long)(s0 + s) * p.Bt.rs, tb + k * 8, p.L, n, p.Bt.vec, w);
-          float4* d = reinterpret_cast<float4*>(Bs + s * TB);
-          d[k] = make_float4(w[0], w[1], w[2], w[3]);
-          d[TL + k] = make_float4(w[4], w[5], w[6], w[7]);
-          load8(Ct + (long long)(s0 + s) * p.Ct.rs, tb + k * 8, p.L, n, p.Ct.vec, w);
-          d = reinterpret_cast<float4*>(Cs + s * TB);
-          d[k] = make_float4(w[0], w[1], w[2], w[3]);
-          d[TL + k] = make_float4(w[4], w[5], w[6], w[7]);
-        }
-        __syncthreads();
-#pragma unroll 2
-        for (int s = 0; s < ns; ++s) {
-          const float A2 = As[(s0 + s) * CH + c];
-          const float4* Bp = reinterpret_cast<const float4*>(Bs + s * TB);
-          const float4* Cp = reinterpret_cast<const float4*>(Cs + s * TB);
-          const float4 b0 = Bp[tl], b1 = Bp[TL + tl];
-          const float Bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-          float a[8], w[8];
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            a[i] = ex2(dt[i] * A2);
-            w[i] = du[i] * Bv[i];
-          }
-          float hh = w[0];
-#pragma unroll
-          for (int i = 1; i < 8; ++i) hh = fmaf(a[i], hh, w[i]);
-          float P = ex2(sum * A2);
-          float x0 = 0.f;
-          if (tl == 0) {
-            x0 = xs[(s0 + s) * CH + c];
-            hh = fmaf(P, x0, hh);
-          }
-#pragma unroll
-          for (int d = 1; d < TL; d *= 2) {  // state at the end of every lane
-            const float hp = __shfl_up_sync(~0u, hh, d, TL);
-            const float Pp = __shfl_up_sync(~0u, P, d, TL);
-            if (tl >= d) {
-              hh = fmaf(P, hp, hh);
-              P *= Pp;
-            }
-          }
-          const float up = __shfl_up_sync(~0u, hh, 1, TL);
-          float x = tl == 0 ? x0 : up;
-          __syncwarp();
-          if (tl == TL - 1) xs[(s0 + s) * CH + c] = hh;
-          if (ckpt && live && (t0 & (kCkptSteps - 1)) == 0 && t0 < n)
-            ckpt[(row * nck + t0 / kCkptSteps) * N + s0 + s] = x;
-          const float4 c0 = Cp[tl], c1 = Cp[TL + tl];
-          const float Cv[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            x = fmaf(a[i], x, w[i]);
-            o[i] = fmaf(Cv[i], x, o[i]);
-          }
-        }
-      }
-      if (z) {
-        float zv[8];
-        load8(z, t0, p.L, n, p.z.vec, zv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) o[i] *= silu(zv[i]);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = 0.f;
+    for (int j = 0; j < VPL; ++j) {
+      const int t0 = k * TB + tl * TPL + j * 8;
+      fetch8(slot((k & 1) * 2, j), u, t0, p.L, n, p.u.vec);
+      fetch8(slot((k & 1) * 2 + 1, j), delta, t0, p.L, n, p.delta.vec);
     }
-    if (live && t0 < p.L) store8(y + row * p.L, t0, p.L, n, p.out_vec, o);
+  };
+  // step sizes of block k: dt = 0 behind the row's end keeps the state
+  auto steps = [&](int k) {
+    l.sum = 0.f;
+#pragma unroll
+    for (int j = 0; j < VPL; ++j) {
+      const int t0 = k * TB + tl * TPL + j * 8;
+      float uv[8], dv[8];
+      take8(slot((k & 1) * 2, j), t0, n, uv);
+      take8(slot((k & 1) * 2 + 1, j), t0, INT_MAX, dv);
+      float2* d = l.dt + 4 * j;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) d[i] = add2(make_float2(dv[2 * i], dv[2 * i + 1]), both(bias));
+      if (p.softplus) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[i] = softplus2(d[i]);
+      }
+      if (t0 + 8 > n) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if (t0 + 2 * i >= n) d[i].x = 0.f;
+          if (t0 + 2 * i + 1 >= n) d[i].y = 0.f;
+        }
+      }
+      float2 sum = add2(add2(d[0], d[1]), add2(d[2], d[3]));
+      l.sum += sum.x + sum.y;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        l.du[4 * j + i] = mul2(d[i], make_float2(uv[2 * i], uv[2 * i + 1]));
+        l.o[4 * j + i] = mul2(both(Dh), make_float2(uv[2 * i], uv[2 * i + 1]));
+      }
+    }
+    if (!OUT) total += l.sum;
+  };
+
+  if (first < end) {
+    next.fetch(p, 0, min(N, kStates), first * TB, n);
+    fetch(first);
+    fetched();
+    next.store(bc, min(N, kStates), first * TB, n);
   }
-  if (state_out) {
-    __syncthreads();
+  __syncthreads();
+  int it = 0;
+  for (int k = first; k < end; ++k) {
+    steps(k);
+    if (OUT && z) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) fetch8(slot(4, j), z, k * TB + tl * TPL + j * 8, p.L, n, p.z.vec);
+    }
+    if (k + 1 < end) fetch(k + 1);
+    float* ck = CKPT ? ckpt + (((long long)b * p.H + h) * nck + k) * N : nullptr;
+    for (int ch = 0; ch < chunks; ++ch, ++it) {
+      const int s0 = ch * kStates, ns = min(N - s0, kStates);
+      const bool more = ch + 1 < chunks || k + 1 < end;
+      const int sn = ch + 1 < chunks ? s0 + kStates : 0, tbn = (ch + 1 < chunks ? k : k + 1) * TB;
+      if (more) next.fetch(p, sn, min(N - sn, kStates), tbn, n);
+      const float* Bs = bc + (it & 1) * 2 * kStates * TB;
+#pragma unroll S::kUnroll
+      for (int e = 0; e < ns; e += SG)
+        run_states<S, OUT, CKPT>(Bs + e * TB, As + (s0 + e) * CH + c, x0s + (s0 + e) * CH, x1s + (s0 + e) * CH * 4, tl,
+                                  l, live && tl == 0, ck + s0 + e, ns - e);
+      fetched();
+      if (more) next.store(bc + ((it + 1) & 1) * 2 * kStates * TB, min(N - sn, kStates), tbn, n);
+      __syncthreads();
+    }
+    if (OUT) {
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const int t0 = k * TB + tl * TPL + j * 8;
+        float v[8], w[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[2 * i] = l.o[4 * j + i].x;
+          v[2 * i + 1] = l.o[4 * j + i].y;
+        }
+        if (z) {
+          take8(slot(4, j), t0, n, w);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= silu(w[i]);
+        }
+        if (live && t0 < p.L) store8(yr, t0, p.L, n, p.out_vec, v);
+      }
+    }
+  }
+  if (OUT) {
+    for (int k = max(first, end); k < last; ++k) {  // behind the row's end
+#pragma unroll
+      for (int j = 0; j < VPL; ++j) {
+        const int t0 = k * TB + tl * TPL + j * 8;
+        float v[8] = {};
+        if (live && t0 < p.L) store8(yr, t0, p.L, n, p.out_vec, v);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int d = 1; d < TL; d *= 2) total += __shfl_xor_sync(~0u, total, d);
+    if (live && tl == 0) sg.dt[((long long)b * p.H + h) * sg.count + seg] = total;
+  }
+  if (!OUT || (state_out && seg == nseg - 1)) {
     for (int i = tid; i < N * CH; i += kThreads) {
       const int cc = i / N, s = i % N;
-      if (tile * CH + cc < E) state_out[((long long)b * p.H + g * E + tile * CH + cc) * N + s] = xs[s * CH + cc];
+      if (tile * CH + cc >= E) continue;
+      const long long row = (long long)b * p.H + g * E + tile * CH + cc;
+      (OUT ? state_out + row * N : sg.state + (row * sg.count + seg) * N)[s] = xs[s * CH + cc];
     }
+  }
+}
+
+// The states entering the segments of a row from their end states, in place.
+__global__ void join_segments_kernel(Segments sg, const float* A, const float* state_in, long long rows, int H, int N) {
+  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= rows * N) return;
+  const long long row = i / N;
+  const int s = (int)(i % N);
+  const float A2 = __ldg(A + row % H * N + s) * kLog2e;
+  float x = state_in ? __ldg(state_in + i) : 0.f;
+  for (int k = 0; k < sg.count; ++k) {
+    float* q = sg.state + (row * sg.count + k) * N + s;
+    const float e = k + 1 < sg.count ? *q : 0.f;
+    *q = x;
+    if (k + 1 < sg.count) x = fmaf(ex2(sg.dt[row * sg.count + k] * A2), x, e);
   }
 }
 
@@ -211,20 +494,71 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs p, float* 
   }
 }
 
-template <typename T, int TL>
-cudaError_t run(const ScanArgs& p, void* y, float* state_out, float* ckpt, cudaStream_t st) {
-  constexpr int CH = kWarps * 32 / TL, TB = TL * 8;
-  const int tiles = (p.H / p.G + CH - 1) / CH;
-  const size_t smem = (size_t)(2 * kStates * TB + 2 * p.N * CH) * 4;
-  const cudaError_t e = smem_optin<scan_kernel<T, TL>>(smem);
+template <typename T, int TPL, int MODE>
+cudaError_t run(const ScanArgs& p, const Segments& sg, void* y, float* state_out, float* ckpt, cudaStream_t st) {
+  constexpr int CH = Shape<TPL>::CH;
+  const int tiles = (p.H / p.G + CH - 1) / CH, nseg = MODE == kEnds ? sg.count - 1 : sg.count;
+  const size_t smem = Layout<T, TPL>::bytes((p.N + kStates - 1) / kStates * kStates);
+  const cudaError_t e = smem_optin<scan_kernel<T, TPL, MODE>>(smem);
   if (e != cudaSuccess) return e;
-  scan_kernel<T, TL><<<(unsigned)((long long)tiles * p.B * p.G), kThreads, smem, st>>>(p, (T*)y, state_out, ckpt, tiles);
+  scan_kernel<T, TPL, MODE><<<(unsigned)((long long)tiles * p.B * p.G * nseg), kThreads, smem, st>>>(
+      p, sg, (T*)y, state_out, ckpt, tiles);
   return cudaGetLastError();
 }
 
+template <typename T, int TPL>
+cudaError_t fwd_t(const ScanArgs& p, const Segments& sg, void* y, float* state_out, float* ckpt, cudaStream_t st) {
+  if (sg.count > 1) {
+    cudaError_t e = run<T, TPL, kEnds>(p, sg, nullptr, nullptr, nullptr, st);
+    if (e != cudaSuccess) return e;
+    const long long rows = (long long)p.B * p.H;
+    join_segments_kernel<<<(unsigned)((rows * p.N + 127) / 128), 128, 0, st>>>(sg, p.A, p.state_in, rows, p.H, p.N);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  return ckpt ? run<T, TPL, kOutputsCkpt>(p, sg, y, state_out, ckpt, st)
+              : run<T, TPL, kOutputs>(p, sg, y, state_out, nullptr, st);
+}
 template <typename T>
-cudaError_t fwd(const ScanArgs& p, void* y, float* state_out, float* ckpt, cudaStream_t st) {
-  return run<T, 8>(p, y, state_out, ckpt, st);
+cudaError_t fwd(const ScanArgs& p, const Segments& sg, void* y, float* state_out, float* ckpt, cudaStream_t st) {
+  return sg.tpl == 8 ? fwd_t<T, 8>(p, sg, y, state_out, ckpt, st) : fwd_t<T, 16>(p, sg, y, state_out, ckpt, st);
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Time of `blocks` 64-step blocks in `ctas` thread blocks, as measured (us, 2048
+// steps of 16 states in 16 bits): c + d r with r thread blocks on an SM, at most four at once.
+float cost(long long ctas, int blocks, float c, float d, int sms) {
+  const long long r = (ctas + sms - 1) / sms, full = r / 4, rest = r % 4;
+  return (full * (c + 4 * d) + (rest ? c + rest * d : 0.f)) * blocks / 32;
+}
+
+// Steps of a lane and segments of a row.  Sixteen steps need the fewest
+// instructions (four thread blocks an SM: 15.4 cycles a warp, state and step,
+// eight: 18.2) but leave half as many warps.  Segments fill the SMs where
+// channels are few, for a first pass of about 0.65 of the work: 128 channels of
+// 8192 steps took 373 us in one piece.  The cheapest of the choices is taken.
+Segments segments(int B, int H, int L, int G) {
+  const int all = (L + TB - 1) / TB, sms = num_sms();
+  Segments best{16, 1, all, nullptr, nullptr};
+  float least = -1.f;
+  for (int tpl = 8; tpl <= 16; tpl += 8) {
+    const int ch = kWarps * 32 / (TB / tpl);
+    const float c = tpl == 8 ? 45.f : 95.f, d = tpl == 8 ? 31.5f : 49.f;
+    const long long ctas = (long long)B * G * ((H / G + ch - 1) / ch);
+    for (int want = 1; want <= 64 && (want == 1 || ctas * (want - 1) < 16 * sms); ++want) {
+      const int blocks = (all + want - 1) / want, count = (all + blocks - 1) / blocks;
+      if (count != want || (count > 1 && blocks < 4)) continue;
+      const float t = cost(ctas * count, blocks, c, d, sms) +
+                      (count > 1 ? 0.65f * cost(ctas * (count - 1), blocks, c, d, sms) + 6.f : 0.f);
+      if (least < 0.f || t < least) {
+        least = t;
+        best.tpl = tpl;
+        best.count = count;
+        best.blocks = blocks;
+      }
+    }
+  }
+  return best;
 }
 
 template <typename T>
@@ -239,12 +573,22 @@ cudaError_t step(const ScanArgs& p, float* state, void* y, const int* slots, int
 
 }  // namespace
 
-cudaError_t launch_selective_scan(const ScanArgs& p, void* y, float* state_out, float* ckpt, int dtype,
+size_t selective_scan_workspace_bytes(int B, int H, int L, int N, int G) {
+  const Segments s = segments(B, H, L, G);
+  return s.count > 1 ? up256((size_t)B * H * s.count * N * 4) + (size_t)B * H * s.count * 4 : 0;
+}
+
+cudaError_t launch_selective_scan(const ScanArgs& p, void* y, float* state_out, float* ckpt, void* workspace, int dtype,
                                   cudaStream_t st) {
+  Segments s = segments(p.B, p.H, p.L, p.G);
+  if (s.count > 1) {
+    s.state = (float*)workspace;
+    s.dt = (float*)((char*)workspace + up256((size_t)p.B * p.H * s.count * p.N * 4));
+  }
   switch (dtype) {
-    case 0: return fwd<float>(p, y, state_out, ckpt, st);
-    case 1: return fwd<__half>(p, y, state_out, ckpt, st);
-    case 2: return fwd<__nv_bfloat16>(p, y, state_out, ckpt, st);
+    case 0: return fwd<float>(p, s, y, state_out, ckpt, st);
+    case 1: return fwd<__half>(p, s, y, state_out, ckpt, st);
+    case 2: return fwd<__nv_bfloat16>(p, s, y, state_out, ckpt, st);
     default: return cudaErrorInvalidValue;
   }
 }

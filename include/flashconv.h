@@ -366,14 +366,19 @@ FC_API fc_status short_conv_step(const void* x, void* state, const float* w, con
  * state_out: B x H x N floats or NULL.  ckpt: selective_scan_ckpt_bytes(...)
  * bytes for selective_scan_bwd (the states entering the 64-step blocks), or
  * NULL.  strides: batch, row of u, delta, z; batch, group, row of Bt, Ct (12).
+ * workspace: selective_scan_workspace(...) bytes, 256-byte aligned (0 bytes,
+ * and then it may be NULL, where the batch and channels fill the GPU; long
+ * sequences of few channels are cut into segments, whose entering states are
+ * found in a first pass).
  * Precision: float32 state and arithmetic (exponentials by the special
  * function unit, relative error about 2^-22), y rounded once. */
 FC_API size_t selective_scan_ckpt_bytes(int B, int H, int L, int N);
+FC_API size_t selective_scan_workspace(int B, int H, int L, int N, int G);
 FC_API fc_status selective_scan_fwd(const void* u, const void* delta, const float* A, const void* Bt, const void* Ct,
                                     const float* D, const float* dt_bias, const void* z, void* y, int B, int H, int L,
                                     int N, int G, int softplus, const int* lengths, const long long* strides,
-                                    const float* state_in, float* state_out, float* ckpt, fc_dtype dtype,
-                                    void* stream);
+                                    const float* state_in, float* state_out, float* ckpt, void* workspace,
+                                    size_t ws_bytes, fc_dtype dtype, void* stream);
 
 /* selective_scan_bwd -- gradients of selective_scan_fwd given dy, the same
  * inputs, the ckpt that it wrote and, or NULL, dstate_out (of state_out).

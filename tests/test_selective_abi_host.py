@@ -79,7 +79,7 @@ def test_short_conv_step_refusals(bad, status, word):
 
 def scan_fwd(**kw):
     a = dict(u=P, delta=P2, A=P3, Bt=P4, Ct=P4 + 4096, D=P3, bias=P3, z=None, y=P5, B=2, H=6, L=40, N=8, G=2, sp=1,
-             lengths=None, strides=None, sin=None, sout=None, ckpt=None, dtype=F16)
+             lengths=None, strides=None, sin=None, sout=None, ckpt=None, ws=None, wsb=0, dtype=F16)
     a.update(kw)
     return _lib.load().selective_scan_fwd(*a.values(), None)
 

@@ -581,7 +581,7 @@ def test_block_trains_and_generates():
     tol = 3 * 2 * (L + 128) * 2.0 ** -21 * 8
     for g, r in zip((gx, gw, gcb, gd, gA, gB, gC, gD, gdtb, gnw, gnb, gz), refs):
         assert float((g.double().cpu() - r).abs().max()) <= tol * float(r.abs().max())
-    assert float((o.double().cpu() - orf).abs().max()) <= tol * float(orf.abs().max())
+    assert float((o.double().cpu() - orf.detach()).abs().max()) <= tol * float(orf.detach().abs().max())
     # generation: six tokens a row from the prompt's states, against one run over prompt and tokens
     for b in range(B):
         n = ns[b]
@@ -672,4 +672,9 @@ def test_offsets_past_31_bits():
     ones = torch.ones(B, 1, 1, L, dtype=torch.float16, device="cuda")
     s, state = api.selective_scan_fwd(x, x, A, ones, ones, return_state=True)
     one, ostate = api.selective_scan_fwd(x[1:, H - 1:], x[1:, H - 1:], A[:1], ones[1:], ones[1:], return_state=True)
-    assert torch.equal(s[1, H - 1], one[0, 0]) and torch.equal(state[1, H - 1], ostate[0, 0])
+    # Other sizes may be cut into other segments, so the bits may differ.  With dt about 0.8 and A = -1 what is more
+    # than 128 steps old is below e^-100; states stay below 10.
+    # Both sides are rounded, half a step (2^-11 in fp16) each: together one step of the value, besides kappa * 10.
+    w = one[0, 0].double()
+    assert bool(((s[1, H - 1].double() - w).abs() <= 2 * 2.0 ** -11 * w.abs() * (1 + kappa(128)) + kappa(128) * 10).all())
+    assert float((state[1, H - 1] - ostate[0, 0]).abs().max()) <= kappa(128) * 10
