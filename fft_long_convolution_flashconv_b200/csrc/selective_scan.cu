@@ -31,49 +31,6 @@ struct Shape {
   static constexpr int SG = TPL == 8 ? 4 : 1, kUnroll = TPL == 8 ? 1 : 4;
 };
 
-__device__ __forceinline__ uint32_t shared_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
-// Eight steps of a row on their way into 8 sizeof(T) bytes of shared memory of
-// the calling thread's own: asynchronous copies where the row's alignment allows
-// them, else through registers (what is at n and behind may come along or not;
-// take8 drops it).
-template <typename T>
-__device__ __forceinline__ void fetch8(T* slot, const T* row, long long t0, int L, int n, bool vec) {
-  if (vec && t0 + 8 <= L) {
-#pragma unroll
-    for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared_addr(slot) + 16 * i),
-                   "l"((const char*)(row + t0) + 16 * i));
-    return;
-  }
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (t0 + i < n)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_addr(slot + i)), "l"(row + t0 + i));
-      else
-        slot[i] = T(0.f);
-  } else if (inner8(t0, L)) {
-    ldraw8_any(row + t0, *reinterpret_cast<Raw8<T>*>(slot));
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) slot[i] = t0 + i < n ? row[t0 + i] : T(0.f);
-  }
-}
-__device__ __forceinline__ void fetched() { asm volatile("cp.async.wait_all;" ::: "memory"); }
-
-// The slot's steps as floats, zeros at n and behind.
-template <typename T>
-__device__ __forceinline__ void take8(const T* slot, long long t0, int n, float (&v)[8]) {
-  Raw8<T> r = *reinterpret_cast<const Raw8<T>*>(slot);
-  unpack8(r, v);
-  if (t0 + 8 > n) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (t0 + i >= n) v[i] = 0.f;
-  }
-}
-
 // Place of step t of a block in a row of the B / C tiles: the first four steps
 // of every lane, then the next four and so on, so that the 16-byte reads of a
 // warp's lanes are contiguous.
@@ -113,15 +70,6 @@ struct Tiles {
   }
 };
 
-// The two words below are read again only behind a block barrier, so the
-// compiler is told of no memory: the next states' loads may pass the store.
-__device__ __forceinline__ void put_shared(uint32_t at, float v) {
-  asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(v));
-}
-__device__ __forceinline__ void put_global(bool on, float* p, float v) {
-  asm volatile("{ .reg .pred q; setp.ne.s32 q, %0, 0; @q st.global.f32 [%1], %2; }" ::"r"((int)on), "l"(p), "f"(v));
-}
-
 // Step D of the scan over a channel's lanes: lane t joins what lane t - D
 // holds, h = P h' + h and P = P P' (not after the last step); lanes below D keep
 // theirs.  One predicated instruction each instead of a branch keeps several
@@ -159,9 +107,8 @@ struct Lane {
 // SG states of a block, rows from Bs on, for a lane's steps: o += C x.  As: the
 // states' A log2(e), rows of CH channels; x0s: the state entering the first lane
 // of a channel, zeros for the others; x1s: where the last lane's end state goes
-// (the others write to a place that nothing reads).  OUT: outputs are wanted,
-// not only states.
-template <typename S, bool OUT, bool CKPT>
+// (the others write to a place that nothing reads).
+template <typename S, bool CKPT>
 __device__ __forceinline__ void run_states(const float* Bs, const float* As, const float* x0s, uint32_t x1s, int tl,
                                            Lane<S::PAIRS>& l, bool keep, float* ckpt, int nlive) {
   constexpr int SG = S::SG, PAIRS = S::PAIRS, TPL = S::TPL, TL = S::TL, CH = S::CH;
@@ -207,7 +154,6 @@ __device__ __forceinline__ void run_states(const float* Bs, const float* As, con
 #pragma unroll
   for (int q = 0; q < SG; ++q) {
     put_shared(x1s + q * CH * 4, h[q]);
-    if (!OUT) continue;
     const float4* Cp = reinterpret_cast<const float4*>(Bs + (kStates + q) * TB) + tl;
     float v = before<TL>(h[q], x0[q]);
     if (CKPT) put_global(keep && q < nlive, ckpt + q, v);
@@ -238,29 +184,14 @@ struct Layout {
   static size_t bytes(int Np) { return (size_t)(states + 4 * Np * CH) * 4; }
 };
 
-// Long sequences of few channels are cut into segments of `seg` 64-step blocks,
-// so that the SMs fill: scan_kernel<kEnds> runs each segment but the last from a
-// zero state and keeps its end state and its sum of dt, join_segments_kernel turns
-// those into the states entering the segments, and the outputs follow segment by
-// segment.
-enum Mode { kOutputs, kOutputsCkpt, kEnds };
-
-struct Segments {
-  int tpl;            // steps of a lane: 8 or 16
-  int count, blocks;  // segments of a row; 64-step blocks of a segment
-  float* state;       // B x H x count x N (null: one segment)
-  float* dt;          // B x H x count
-};
-
 // A block of four warps takes CH channels of a group.
-template <typename T, int TPL, int MODE>
+template <typename T, int TPL, bool CKPT>
 __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, Segments sg, T* y,
                                                                                 float* state_out, float* ckpt,
                                                                                 int tiles) {
   using S = Shape<TPL>;
   using Sm = Layout<T, TPL>;
   constexpr int TL = S::TL, CL = S::CL, CH = S::CH, VPL = S::VPL, SG = S::SG;
-  constexpr bool OUT = MODE != kEnds, CKPT = MODE == kOutputsCkpt;
   static_assert(kStates % SG == 0, "states come in whole groups");
   extern __shared__ float4 smem4[];
   float* const sm = reinterpret_cast<float*>(smem4);
@@ -269,7 +200,7 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, 
   float* const As = sm + Sm::states;
   float* const xs = As + Np * CH;
   const int tid = threadIdx.x, lane = tid & 31, tl = lane % TL, c = (tid >> 5) * CL + lane / TL;
-  const int E = p.H / p.G, nseg = OUT ? sg.count : sg.count - 1;
+  const int E = p.H / p.G, nseg = sg.count;
   const int seg = blockIdx.x % nseg, tile = blockIdx.x / nseg % tiles, bg = blockIdx.x / nseg / tiles;
   const int b = bg / p.G, g = bg % p.G;
   const int n = row_length(p.lengths, b, p.L);
@@ -278,9 +209,10 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, 
     const bool ok = tile * CH + cc < E && s < N;
     const long long row = (long long)b * p.H + hh;
     As[i] = ok ? __ldg(p.A + (long long)hh * N + s) * kLog2e : 0.f;
-    xs[i] = !ok || !OUT ? 0.f
-            : sg.state  ? sg.state[(row * sg.count + seg) * N + s]
-            : p.state_in ? __ldg(p.state_in + row * N + s) : 0.f;
+    xs[i] = !ok          ? 0.f
+            : sg.state   ? __ldg(sg.state + (row * nseg + seg) * N + s)
+            : p.state_in ? __ldg(p.state_in + row * N + s)
+                         : 0.f;
     xs[Np * CH + i] = 0.f;
   }
   const float* const x0s = (tl == 0 ? xs : xs + Np * CH) + c;
@@ -288,7 +220,6 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, 
   const bool live = tile * CH + c < E;
   const int h = g * E + (live ? tile * CH + c : 0);
   const float Dh = p.D ? __ldg(p.D + h) : 0.f, bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
-  float total = 0.f;
   const T* u = (const T*)p.u.p + b * p.u.bs + h * p.u.rs;
   const T* delta = (const T*)p.delta.p + b * p.delta.bs + h * p.delta.rs;
   const T* z = p.z.p ? (const T*)p.z.p + b * p.z.bs + h * p.z.rs : nullptr;
@@ -341,7 +272,6 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, 
         l.o[4 * j + i] = mul2(both(Dh), make_float2(uv[2 * i], uv[2 * i + 1]));
       }
     }
-    if (!OUT) total += l.sum;
   };
 
   if (first < end) {
@@ -354,7 +284,7 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, 
   int it = 0;
   for (int k = first; k < end; ++k) {
     steps(k);
-    if (OUT && z) {
+    if (z) {
 #pragma unroll
       for (int j = 0; j < VPL; ++j) fetch8(slot(4, j), z, k * TB + tl * TPL + j * 8, p.L, n, p.z.vec);
     }
@@ -368,68 +298,42 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, 
       const float* Bs = bc + (it & 1) * 2 * kStates * TB;
 #pragma unroll S::kUnroll
       for (int e = 0; e < ns; e += SG)
-        run_states<S, OUT, CKPT>(Bs + e * TB, As + (s0 + e) * CH + c, x0s + (s0 + e) * CH, x1s + (s0 + e) * CH * 4, tl,
+        run_states<S, CKPT>(Bs + e * TB, As + (s0 + e) * CH + c, x0s + (s0 + e) * CH, x1s + (s0 + e) * CH * 4, tl,
                                   l, live && tl == 0, ck + s0 + e, ns - e);
       fetched();
       if (more) next.store(bc + ((it + 1) & 1) * 2 * kStates * TB, min(N - sn, kStates), tbn, n);
       __syncthreads();
     }
-    if (OUT) {
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        const int t0 = k * TB + tl * TPL + j * 8;
-        float v[8], w[8];
+    for (int j = 0; j < VPL; ++j) {
+      const int t0 = k * TB + tl * TPL + j * 8;
+      float v[8], w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          v[2 * i] = l.o[4 * j + i].x;
-          v[2 * i + 1] = l.o[4 * j + i].y;
-        }
-        if (z) {
-          take8(slot(4, j), t0, n, w);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) v[i] *= silu(w[i]);
-        }
-        if (live && t0 < p.L) store8(yr, t0, p.L, n, p.out_vec, v);
+      for (int i = 0; i < 4; ++i) {
+        v[2 * i] = l.o[4 * j + i].x;
+        v[2 * i + 1] = l.o[4 * j + i].y;
       }
+      if (z) {
+        take8(slot(4, j), t0, n, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] *= silu(w[i]);
+      }
+      if (live && t0 < p.L) store8(yr, t0, p.L, n, p.out_vec, v);
     }
   }
-  if (OUT) {
-    for (int k = max(first, end); k < last; ++k) {  // behind the row's end
+  for (int k = max(first, end); k < last; ++k) {  // behind the row's end
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) {
-        const int t0 = k * TB + tl * TPL + j * 8;
-        float v[8] = {};
-        if (live && t0 < p.L) store8(yr, t0, p.L, n, p.out_vec, v);
-      }
+    for (int j = 0; j < VPL; ++j) {
+      const int t0 = k * TB + tl * TPL + j * 8;
+      float v[8] = {};
+      if (live && t0 < p.L) store8(yr, t0, p.L, n, p.out_vec, v);
     }
-  } else {
-#pragma unroll
-    for (int d = 1; d < TL; d *= 2) total += __shfl_xor_sync(~0u, total, d);
-    if (live && tl == 0) sg.dt[((long long)b * p.H + h) * sg.count + seg] = total;
   }
-  if (!OUT || (state_out && seg == nseg - 1)) {
+  if (state_out && seg == nseg - 1) {
     for (int i = tid; i < N * CH; i += kThreads) {
       const int cc = i / N, s = i % N;
-      if (tile * CH + cc >= E) continue;
-      const long long row = (long long)b * p.H + g * E + tile * CH + cc;
-      (OUT ? state_out + row * N : sg.state + (row * sg.count + seg) * N)[s] = xs[s * CH + cc];
+      if (tile * CH + cc < E) state_out[((long long)b * p.H + g * E + tile * CH + cc) * N + s] = xs[s * CH + cc];
     }
-  }
-}
-
-// The states entering the segments of a row from their end states, in place.
-__global__ void join_segments_kernel(Segments sg, const float* A, const float* state_in, long long rows, int H, int N) {
-  const long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= rows * N) return;
-  const long long row = i / N;
-  const int s = (int)(i % N);
-  const float A2 = __ldg(A + row % H * N + s) * kLog2e;
-  float x = state_in ? __ldg(state_in + i) : 0.f;
-  for (int k = 0; k < sg.count; ++k) {
-    float* q = sg.state + (row * sg.count + k) * N + s;
-    const float e = k + 1 < sg.count ? *q : 0.f;
-    *q = x;
-    if (k + 1 < sg.count) x = fmaf(ex2(sg.dt[row * sg.count + k] * A2), x, e);
   }
 }
 
@@ -494,52 +398,39 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs p, float* 
   }
 }
 
-template <typename T, int TPL, int MODE>
+template <typename T, int TPL, bool CKPT>
 cudaError_t run(const ScanArgs& p, const Segments& sg, void* y, float* state_out, float* ckpt, cudaStream_t st) {
   constexpr int CH = Shape<TPL>::CH;
-  const int tiles = (p.H / p.G + CH - 1) / CH, nseg = MODE == kEnds ? sg.count - 1 : sg.count;
+  const int tiles = (p.H / p.G + CH - 1) / CH;
   const size_t smem = Layout<T, TPL>::bytes((p.N + kStates - 1) / kStates * kStates);
-  const cudaError_t e = smem_optin<scan_kernel<T, TPL, MODE>>(smem);
+  const cudaError_t e = smem_optin<scan_kernel<T, TPL, CKPT>>(smem);
   if (e != cudaSuccess) return e;
-  scan_kernel<T, TPL, MODE><<<(unsigned)((long long)tiles * p.B * p.G * nseg), kThreads, smem, st>>>(
+  scan_kernel<T, TPL, CKPT><<<(unsigned)((long long)tiles * p.B * p.G * sg.count), kThreads, smem, st>>>(
       p, sg, (T*)y, state_out, ckpt, tiles);
   return cudaGetLastError();
 }
 
-template <typename T, int TPL>
-cudaError_t fwd_t(const ScanArgs& p, const Segments& sg, void* y, float* state_out, float* ckpt, cudaStream_t st) {
-  if (sg.count > 1) {
-    cudaError_t e = run<T, TPL, kEnds>(p, sg, nullptr, nullptr, nullptr, st);
-    if (e != cudaSuccess) return e;
-    const long long rows = (long long)p.B * p.H;
-    join_segments_kernel<<<(unsigned)((rows * p.N + 127) / 128), 128, 0, st>>>(sg, p.A, p.state_in, rows, p.H, p.N);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  }
-  return ckpt ? run<T, TPL, kOutputsCkpt>(p, sg, y, state_out, ckpt, st)
-              : run<T, TPL, kOutputs>(p, sg, y, state_out, nullptr, st);
-}
 template <typename T>
-cudaError_t fwd(const ScanArgs& p, const Segments& sg, void* y, float* state_out, float* ckpt, cudaStream_t st) {
-  return sg.tpl == 8 ? fwd_t<T, 8>(p, sg, y, state_out, ckpt, st) : fwd_t<T, 16>(p, sg, y, state_out, ckpt, st);
+cudaError_t fwd(const ScanArgs& p, int tpl, const Segments& sg, void* y, float* state_out, float* ckpt,
+                cudaStream_t st) {
+  if (tpl == 8)
+    return ckpt ? run<T, 8, true>(p, sg, y, state_out, ckpt, st) : run<T, 8, false>(p, sg, y, state_out, nullptr, st);
+  return ckpt ? run<T, 16, true>(p, sg, y, state_out, ckpt, st) : run<T, 16, false>(p, sg, y, state_out, nullptr, st);
 }
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
-// Time of `blocks` 64-step blocks in `ctas` thread blocks, as measured (us, 2048
-// steps of 16 states in 16 bits): c + d r with r thread blocks on an SM, at most four at once.
-float cost(long long ctas, int blocks, float c, float d, int sms) {
-  const long long r = (ctas + sms - 1) / sms, full = r / 4, rest = r % 4;
-  return (full * (c + 4 * d) + (rest ? c + rest * d : 0.f)) * blocks / 32;
-}
+struct Plan {
+  int tpl;
+  Segments sg;
+};
 
 // Steps of a lane and segments of a row.  Sixteen steps need the fewest
 // instructions (four thread blocks an SM: 15.4 cycles a warp, state and step,
 // eight: 18.2) but leave half as many warps.  Segments fill the SMs where
-// channels are few, for a first pass of about 0.65 of the work: 128 channels of
+// channels are few, for a first pass over the segments' end states: 128 channels of
 // 8192 steps took 373 us in one piece.  The cheapest of the choices is taken.
-Segments segments(int B, int H, int L, int G) {
+Plan plan(int B, int H, int L, int N, int G) {
   const int all = (L + TB - 1) / TB, sms = num_sms();
-  Segments best{16, 1, all, nullptr, nullptr};
+  Plan best{16, {1, all, nullptr, nullptr}};
   float least = -1.f;
   for (int tpl = 8; tpl <= 16; tpl += 8) {
     const int ch = kWarps * 32 / (TB / tpl);
@@ -548,13 +439,11 @@ Segments segments(int B, int H, int L, int G) {
     for (int want = 1; want <= 64 && (want == 1 || ctas * (want - 1) < 16 * sms); ++want) {
       const int blocks = (all + want - 1) / want, count = (all + blocks - 1) / blocks;
       if (count != want || (count > 1 && blocks < 4)) continue;
-      const float t = cost(ctas * count, blocks, c, d, sms) +
-                      (count > 1 ? 0.65f * cost(ctas * (count - 1), blocks, c, d, sms) + 6.f : 0.f);
+      const float t = scan_cost(ctas * count, blocks, kMinBlocks, c, d, sms) +
+                      (count > 1 ? ends_cost(B, H, G, N, count, blocks, sms) : 0.f);
       if (least < 0.f || t < least) {
         least = t;
-        best.tpl = tpl;
-        best.count = count;
-        best.blocks = blocks;
+        best = {tpl, {count, blocks, nullptr, nullptr}};
       }
     }
   }
@@ -574,21 +463,21 @@ cudaError_t step(const ScanArgs& p, float* state, void* y, const int* slots, int
 }  // namespace
 
 size_t selective_scan_workspace_bytes(int B, int H, int L, int N, int G) {
-  const Segments s = segments(B, H, L, G);
-  return s.count > 1 ? up256((size_t)B * H * s.count * N * 4) + (size_t)B * H * s.count * 4 : 0;
+  return segments_bytes(plan(B, H, L, N, G).sg, B, H, N);
 }
 
 cudaError_t launch_selective_scan(const ScanArgs& p, void* y, float* state_out, float* ckpt, void* workspace, int dtype,
                                   cudaStream_t st) {
-  Segments s = segments(p.B, p.H, p.L, p.G);
-  if (s.count > 1) {
-    s.state = (float*)workspace;
-    s.dt = (float*)((char*)workspace + up256((size_t)p.B * p.H * s.count * p.N * 4));
+  Plan pl = plan(p.B, p.H, p.L, p.N, p.G);
+  place_segments(&pl.sg, workspace, p.B, p.H, p.N);
+  if (pl.sg.count > 1) {
+    const cudaError_t e = launch_segment_states(p, pl.sg, p.state_in, false, dtype, st);
+    if (e != cudaSuccess) return e;
   }
   switch (dtype) {
-    case 0: return fwd<float>(p, s, y, state_out, ckpt, st);
-    case 1: return fwd<__half>(p, s, y, state_out, ckpt, st);
-    case 2: return fwd<__nv_bfloat16>(p, s, y, state_out, ckpt, st);
+    case 0: return fwd<float>(p, pl.tpl, pl.sg, y, state_out, ckpt, st);
+    case 1: return fwd<__half>(p, pl.tpl, pl.sg, y, state_out, ckpt, st);
+    case 2: return fwd<__nv_bfloat16>(p, pl.tpl, pl.sg, y, state_out, ckpt, st);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -7,14 +7,20 @@
 //   dA_n = sum_{b,t} dt g_n a_n x_n[t-1],  dD = sum dyp u,  ddt_bias = sum ddelta
 //   dB_n[t] = sum_h g_n dt u,  dC_n[t] = sum_h dyp x_n,  dz = dy y silu'(z)
 //
-// A warp takes four channels by 64 steps (eight lanes of eight steps a
-// channel) and walks through the 64-step blocks from the last to the first.
-// In a block it runs each state forward again from the kept state that enters
-// the block, then its adjoint backward; both recurrences are joined over a
-// channel's lanes by shuffles.  dB and dC are summed over the warp's channels
-// by shuffles, over the block's warps in shared memory and over the blocks by
-// scan_sum_kernel, always in the same order, so results do not change from
-// run to run.
+// A lane holds eight steps of one channel; eight lanes are a channel's 64-step
+// block, a warp takes four channels and walks through the blocks from the last
+// to the first.  In a block it runs each state forward again from the kept state
+// that enters the block, then its adjoint backward; both recurrences are joined
+// over a channel's lanes by shuffles, as in the forward kernel.
+//
+// dB and dC are sums over the group's channels: shuffles add the four lanes that
+// hold the same steps (each keeps a quarter of them), the block's warps are added
+// in shared memory and the blocks by scan_sum_bc_kernel, always in the same order,
+// so results do not change from run to run.  (Adding up the lanes by products with
+// ones on the tensor cores cost more instructions, most of them moves into operand
+// registers; two channels a lane would halve the shuffles but spill at the 168
+// registers that three blocks an SM leave: 1556 and 1799 us against 1537 for a
+// training step of 4 x 1024 channels of 8192 steps.)
 #include "kernels.cuh"
 #include "scan.cuh"
 
@@ -23,9 +29,10 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStates = 16;  // states whose tiles are in shared memory at a time
-constexpr int TL = 8, CL = 4, TB = kCkptSteps, CH = kWarps * CL;
-static_assert(TB == TL * 8, "a block of steps is what a channel's lanes hold");
+constexpr int kStates = 8;  // states whose tiles are in shared memory at a time
+constexpr int kMinBlocks = 4;  // resident on an SM: 128 registers a thread
+constexpr int TPL = 8, TL = 8, CL = 4, TB = kCkptSteps, CH = kWarps * CL, PAIRS = TPL / 2;
+static_assert(TB == TL * TPL, "a block of steps is what a channel's lanes hold");
 
 struct BwdOut {
   void *du, *ddelta, *dz;
@@ -33,54 +40,110 @@ struct BwdOut {
   const float* dstate_out;
   float* dstate_in;
   float* part_bc;  // [tiles][2][B][G][N][L]
-  float* part_a;   // [B][H][N]
-  float* part_d;   // [B][H] dD, then [B][H] ddt_bias
+  float* part_a;   // [B][segments][H][N]
+  float* part_d;   // [2][B][segments][H]: dD, ddt_bias
 };
 
-// Sum v over the four lanes lane ^ 8, lane ^ 16: lane (cl, tl) returns the sums
-// of elements 2 cl and 2 cl + 1 of the eight.
-__device__ __forceinline__ float2 sum_channels(const float (&v)[8], int cl) {
-  float w[4];
-  const bool hi = cl & 2, odd = cl & 1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float give = hi ? v[i] : v[i + 4], keep = hi ? v[i + 4] : v[i];
-    w[i] = keep + __shfl_xor_sync(~0u, give, 16);
+// Step D of the scan over a channel's lanes, which are four lanes apart: from the
+// lanes before (UP) or behind.
+template <bool UP, int D>
+__device__ __forceinline__ void join(float& h, float& P) {
+  if constexpr (D * 2 == TL) {  // the product is not needed after the last step
+    if constexpr (UP)
+      asm volatile("{ .reg .pred q; .reg .f32 t; shfl.sync.up.b32 t|q, %0, %2, 0, -1; @q fma.rn.f32 %0, %1, t, %0; }"
+                   : "+f"(h)
+                   : "f"(P), "n"(D * CL));
+    else
+      asm volatile("{ .reg .pred q; .reg .f32 t; shfl.sync.down.b32 t|q, %0, %2, 31, -1; @q fma.rn.f32 %0, %1, t, %0; }"
+                   : "+f"(h)
+                   : "f"(P), "n"(D * CL));
+  } else if constexpr (UP) {
+    asm volatile(
+        "{ .reg .pred q; .reg .f32 t, s; shfl.sync.up.b32 t|q, %0, %2, 0, -1; shfl.sync.up.b32 s, %1, %2, 0, -1;\n"
+        "@q fma.rn.f32 %0, %1, t, %0; @q mul.rn.f32 %1, %1, s; }"
+        : "+f"(h), "+f"(P)
+        : "n"(D * CL));
+  } else {
+    asm volatile(
+        "{ .reg .pred q; .reg .f32 t, s; shfl.sync.down.b32 t|q, %0, %2, 31, -1; shfl.sync.down.b32 s, %1, %2, 31, -1;\n"
+        "@q fma.rn.f32 %0, %1, t, %0; @q mul.rn.f32 %1, %1, s; }"
+        : "+f"(h), "+f"(P)
+        : "n"(D * CL));
   }
-  float r[2];
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float give = odd ? w[i] : w[i + 2], keep = odd ? w[i + 2] : w[i];
-    r[i] = keep + __shfl_xor_sync(~0u, give, 8);
-  }
-  return make_float2(r[0], r[1]);
+}
+// The neighbour's h; the first (last) lane of a channel keeps `edge`.
+template <bool UP>
+__device__ __forceinline__ float neighbour(float h, float edge) {
+  if constexpr (UP)
+    asm volatile("{ .reg .pred q; .reg .f32 t; shfl.sync.up.b32 t|q, %1, %2, 0, -1; @q mov.f32 %0, t; }"
+                 : "+f"(edge)
+                 : "f"(h), "n"(CL));
+  else
+    asm volatile("{ .reg .pred q; .reg .f32 t; shfl.sync.down.b32 t|q, %1, %2, 31, -1; @q mov.f32 %0, t; }"
+                 : "+f"(edge)
+                 : "f"(h), "n"(CL));
+  return edge;
 }
 
+// Sum v (eight steps) over the four lanes that hold the same steps, lane ^ 1 and
+// lane ^ 2: lane 4 tl + cl returns the sums of elements 2 cl and 2 cl + 1.
+__device__ __forceinline__ float2 sum_channels(const float2 (&v)[PAIRS], int cl) {
+  const bool hi = cl & 2, odd = cl & 1;
+  float2 w[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float2 give = hi ? v[i] : v[i + 2], keep = hi ? v[i + 2] : v[i];
+    w[i] = add2(keep, make_float2(__shfl_xor_sync(~0u, give.x, 2), __shfl_xor_sync(~0u, give.y, 2)));
+  }
+  const float2 give = odd ? w[0] : w[1], keep = odd ? w[1] : w[0];
+  return add2(keep, make_float2(__shfl_xor_sync(~0u, give.x, 1), __shfl_xor_sync(~0u, give.y, 1)));
+}
+
+// Place of step t in a row of the B / C tiles: the first four steps of every
+// lane, then the others, so that the 16-byte reads of a warp's lanes are contiguous.
+__device__ __forceinline__ int tile_at(int t) { return (t & 4) * TL + (t >> 3) * 4 + (t & 3); }
+
 template <typename T>
-__global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanArgs p, BwdOut q, int tiles) {
+struct Sm {
+  T in[2][4][kThreads][8];                          // u, delta, dy, z of even and odd blocks
+  T raw[kStates * TB / 8 * 2 / kThreads][kThreads][8];  // B and C on their way
+  float tile[2][2][kStates][TB];                    // B and C as floats
+  float sums[kWarps][kStates][2][TB];               // dB, dC of a warp's channels
+  float ck[2][kStates][CH];                         // states entering the block
+  float zero[kStates][CH];                          // for the lanes that none enters
+  // [Np][CH] each: A, dA, what nothing reads, entering adjoint, what nothing reads
+};
+
+template <typename T>
+__global__ __launch_bounds__(kThreads, kMinBlocks) void scan_bwd_kernel(ScanArgs p, BwdOut q, Segments sg, int tiles) {
   extern __shared__ float4 smem4[];
-  float* Bs = reinterpret_cast<float*>(smem4);  // [kStates][TB]
-  float* Cs = Bs + kStates * TB;
-  float* wb = Cs + kStates * TB;                    // [kWarps][kStates][2][TB] dB, dC of a warp's channels
-  float* As = wb + kWarps * kStates * 2 * TB;       // [N][CH]
-  float* gs = As + p.N * CH;                        // [N][CH] a g of the first step behind the block
-  float* das = gs + p.N * CH;                       // [N][CH] dA
-  const int tid = threadIdx.x, lane = tid & 31, tl = lane % TL, cl = lane / TL, warp = tid >> 5;
-  const int c = warp * CL + cl;
+  Sm<T>& sm = *reinterpret_cast<Sm<T>*>(smem4);
+  const int N = p.N, chunks = (N + kStates - 1) / kStates, Np = chunks * kStates;
+  float* const As = reinterpret_cast<float*>(&sm + 1);  // [Np][CH]
+  float* const das = As + Np * CH;                      // as large each, and as much behind them that nothing reads
+  float* const gs = das + 2 * Np * CH;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tl = lane / CL, cl = lane % CL, c = warp * CL + cl;
   const int E = p.H / p.G;
-  const int tile = blockIdx.x % tiles, bg = blockIdx.x / tiles, b = bg / p.G, g = bg % p.G;
+  const int seg = blockIdx.x % sg.count, tile = blockIdx.x / sg.count % tiles, bg = blockIdx.x / sg.count / tiles;
+  const int b = bg / p.G, g = bg % p.G;
   const bool live = tile * CH + c < E;
   const int h = g * E + (live ? tile * CH + c : 0);
   const long long row = (long long)b * p.H + h;
   const int n = row_length(p.lengths, b, p.L);
-  const int N = p.N;
-  for (int i = tid; i < N * CH; i += kThreads) {
+  for (int i = tid; i < Np * CH; i += kThreads) {
     const int s = i / CH, cc = i % CH, hh = g * E + tile * CH + cc;
-    const bool ok = tile * CH + cc < E;
+    const bool ok = tile * CH + cc < E && s < N;
+    const long long r = (long long)b * p.H + hh;
     As[i] = ok ? __ldg(p.A + (long long)hh * N + s) : 0.f;
-    gs[i] = ok && q.dstate_out ? __ldg(q.dstate_out + ((long long)b * p.H + hh) * N + s) : 0.f;
-    das[i] = 0.f;
+    gs[i] = !ok            ? 0.f
+            : sg.state     ? __ldg(sg.state + (r * sg.count + seg) * N + s)
+            : q.dstate_out ? __ldg(q.dstate_out + r * N + s)
+                           : 0.f;
+    das[i] = das[Np * CH + i] = 0.f;
+    if (i < kStates * CH) sm.zero[0][i] = 0.f;
   }
+  float* const da_at = das + (tl == 0 ? 0 : Np * CH) + c;
+  const uint32_t r1s = shared_addr(tl == 0 ? gs + c : gs + Np * CH + c);
   const T* u = (const T*)p.u.p + b * p.u.bs + h * p.u.rs;
   const T* delta = (const T*)p.delta.p + b * p.delta.bs + h * p.delta.rs;
   const T* dy = (const T*)p.dy.p + b * p.dy.bs + h * p.dy.rs;
@@ -89,199 +152,260 @@ __global__ __launch_bounds__(kThreads) void scan_bwd_kernel(ScanArgs p, BwdOut q
   const T* Ct = (const T*)p.Ct.p + b * p.Ct.bs + g * p.Ct.gs;
   const float Dh = p.D ? __ldg(p.D + h) : 0.f, bias = p.dt_bias ? __ldg(p.dt_bias + h) : 0.f;
   const int nck = (p.L + TB - 1) / TB;
+  const int first = seg * sg.blocks, last = min(nck, first + sg.blocks), end = min(last, (n + TB - 1) / TB);
   float* pbc = q.part_bc + ((long long)tile * 2 * p.B * p.G + bg) * N * p.L;  // dB; dC is B G N L further
   const long long pstep = (long long)p.B * p.G * N * p.L;
+
+  for (int k = max(first, end); k < last; ++k) {  // behind the row's end
+    const int t0 = k * TB + tl * 8;
+    float o[8] = {};
+    if (live && t0 < p.L) {
+      store8((T*)q.du + row * p.L, t0, p.L, n, p.out_vec, o);
+      store8((T*)q.ddelta + row * p.L, t0, p.L, n, p.out_vec, o);
+      if (z) store8((T*)q.dz + row * p.L, t0, p.L, n, p.out_vec, o);
+    }
+    for (int i = tid; i < N * TB; i += kThreads) {
+      const int t = k * TB + i % TB;
+      if (t < p.L) {
+        pbc[(long long)(i / TB) * p.L + t] = 0.f;
+        pbc[pstep + (long long)(i / TB) * p.L + t] = 0.f;
+      }
+    }
+  }
+
+  auto fetch = [&](int k) {
+    const int t0 = k * TB + tl * 8, m = live ? n : 0;
+    fetch8(sm.in[k & 1][0][tid], u, t0, p.L, m, p.u.vec);
+    fetch8(sm.in[k & 1][1][tid], delta, t0, p.L, m, p.delta.vec);
+    fetch8(sm.in[k & 1][2][tid], dy, t0, p.L, m, p.dy.vec);
+    if (z) fetch8(sm.in[k & 1][3][tid], z, t0, p.L, m, p.z.vec);
+  };
+  constexpr int kRow = TB / 8, kPer = kStates * kRow * 2 / kThreads;
+  static_assert(kStates * kRow * 2 % kThreads == 0 && kStates * CH == kThreads, "whole vectors and words a thread");
+  // B, C and entering states of chunk ch of block k, the it-th in order
+  auto fetch_tile = [&](int k, int ch, int it) {
+    const int s0 = ch * kStates;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int v = tid + j * kThreads, s = s0 + v / kRow % kStates, t0 = k * TB + v % kRow * 8;
+      const bool second = v >= kStates * kRow;
+      if (s < N)
+        fetch8(sm.raw[j][tid], (second ? Ct : Bt) + s * (second ? p.Ct.rs : p.Bt.rs), t0, p.L, n,
+               second ? p.Ct.vec : p.Bt.vec);
+    }
+    const int s = s0 + tid % kStates, cc = tid / kStates;
+    float* d = &sm.ck[it & 1][tid % kStates][cc];
+    if (s < N && tile * CH + cc < E)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_addr(d)),
+                   "l"(q.ckpt + (((long long)b * p.H + g * E + tile * CH + cc) * nck + k) * N + s));
+    else
+      *d = 0.f;
+  };
+  auto commit_tile = [&](int k, int ch, int it) {
+    fetched();
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int v = tid + j * kThreads, s = v / kRow % kStates, t = v % kRow * 8;
+      float w[8] = {};
+      if (ch * kStates + s < N) take8(sm.raw[j][tid], k * TB + t, n, w);
+      float* d = sm.tile[it & 1][v >= kStates * kRow][s];
+      *reinterpret_cast<float4*>(d + tile_at(t)) = make_float4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<float4*>(d + tile_at(t + 4)) = make_float4(w[4], w[5], w[6], w[7]);
+    }
+  };
+  if (first < end) {
+    fetch(end - 1);
+    fetch_tile(end - 1, 0, 0);
+    commit_tile(end - 1, 0, 0);
+  }
+  __syncthreads();
   float sum_d = 0.f, sum_bias = 0.f;
-  for (int k = nck - 1; k >= 0; --k) {
-    const int tb = k * TB, t0 = tb + tl * 8;
-    if (tb >= n) {
-      float o[8] = {};
-      if (live && t0 < p.L) {
-        store8((T*)q.du + row * p.L, t0, p.L, n, p.out_vec, o);
-        store8((T*)q.ddelta + row * p.L, t0, p.L, n, p.out_vec, o);
-        if (z) store8((T*)q.dz + row * p.L, t0, p.L, n, p.out_vec, o);
-      }
-      for (int i = tid; i < N * TB; i += kThreads) {
-        const int t = tb + i % TB;
-        if (t < p.L) {
-          pbc[(long long)(i / TB) * p.L + t] = 0.f;
-          pbc[pstep + (long long)(i / TB) * p.L + t] = 0.f;
-        }
-      }
-      continue;
-    }
-    float dt[8], du[8], dyp[8], gB[8], gA[8], y0[8], sum = 0.f;
+  int it = 0;
+  for (int k = end - 1; k >= first; --k) {
+    const int t0 = k * TB + tl * 8, m = live ? n : 0;
+    float2 dt[PAIRS], du[PAIRS], dyp[PAIRS], gB[PAIRS], gA[PAIRS], y0[PAIRS];
+    float sum;
     {
-      float v[8];
-      load8(u, t0, p.L, live ? n : 0, p.u.vec, v);
-      load8(delta, t0, p.L, n, p.delta.vec, dt);
-      load8(dy, t0, p.L, live ? n : 0, p.dy.vec, dyp);
+      float v[8], d[8], e[8];
+      take8(sm.in[k & 1][0][tid], t0, m, v);
+      take8(sm.in[k & 1][1][tid], t0, INT_MAX, d);
+      take8(sm.in[k & 1][2][tid], t0, m, e);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float r = dt[i] + bias;
-        dt[i] = t0 + i < n ? (p.softplus ? softplus(r) : r) : 0.f;
-        sum += dt[i];
-        du[i] = dt[i] * v[i];
-        y0[i] = Dh * v[i];
-        gB[i] = gA[i] = 0.f;
+      for (int i = 0; i < PAIRS; ++i) dt[i] = add2(make_float2(d[2 * i], d[2 * i + 1]), both(bias));
+      if (p.softplus) {
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) dt[i] = softplus2(dt[i]);
       }
-      if (z) {
-        load8(z, t0, p.L, n, p.z.vec, v);
+      if (t0 + 8 > n) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) dyp[i] *= silu(v[i]);
+        for (int i = 0; i < PAIRS; ++i) {
+          if (t0 + 2 * i >= n) dt[i].x = 0.f;
+          if (t0 + 2 * i + 1 >= n) dt[i].y = 0.f;
+        }
+      }
+      const float2 s2 = add2(add2(dt[0], dt[1]), add2(dt[2], dt[3]));
+      sum = s2.x + s2.y;
+      if (z) {
+        take8(sm.in[k & 1][3][tid], t0, m, d);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] *= silu(d[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < PAIRS; ++i) {
+        const float2 uv = make_float2(v[2 * i], v[2 * i + 1]);
+        du[i] = mul2(dt[i], uv);
+        y0[i] = mul2(both(Dh), uv);
+        dyp[i] = make_float2(e[2 * i], e[2 * i + 1]);
+        gB[i] = gA[i] = make_float2(0.f, 0.f);
       }
     }
-    for (int s0 = 0; s0 < N; s0 += kStates) {
-      const int ns = min(kStates, N - s0);
-      __syncthreads();
-      for (int i = tid; i < ns * TL; i += kThreads) {
-        const int s = i / TL, j = i % TL;
-        float w[8];
-        load8(Bt + (s0 + s) * p.Bt.rs, tb + j * 8, p.L, n, p.Bt.vec, w);
-        float4* d = reinterpret_cast<float4*>(Bs + s * TB);
-        d[j] = make_float4(w[0], w[1], w[2], w[3]);
-        d[TL + j] = make_float4(w[4], w[5], w[6], w[7]);
-        load8(Ct + (s0 + s) * p.Ct.rs, tb + j * 8, p.L, n, p.Ct.vec, w);
-        d = reinterpret_cast<float4*>(Cs + s * TB);
-        d[j] = make_float4(w[0], w[1], w[2], w[3]);
-        d[TL + j] = make_float4(w[4], w[5], w[6], w[7]);
-      }
-      __syncthreads();
+    if (k > first) fetch(k - 1);
+    for (int ch = 0; ch < chunks; ++ch, ++it) {
+      const int s0 = ch * kStates, ns = min(N - s0, kStates);
+      const bool more = ch + 1 < chunks || k > first;
+      const int kn = ch + 1 < chunks ? k : k - 1, cn = ch + 1 < chunks ? ch + 1 : 0;
+      if (more) fetch_tile(kn, cn, it + 1);
+      const float* xin = tl == 0 ? &sm.ck[it & 1][0][c] : &sm.zero[0][c];
+      const float* rin = tl == TL - 1 ? gs + s0 * CH + c : &sm.zero[0][c];
+#pragma unroll 1
       for (int s = 0; s < ns; ++s) {
-        const float An = As[(s0 + s) * CH + c], A2 = An * kLog2e;
-        const float4* Bp = reinterpret_cast<const float4*>(Bs + s * TB);
-        const float4* Cp = reinterpret_cast<const float4*>(Cs + s * TB);
-        const float4 b0 = Bp[tl], b1 = Bp[TL + tl], c0 = Cp[tl], c1 = Cp[TL + tl];
-        const float Bv[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
-        const float Cv[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        float a[8], ax[8], r[8];
+        const float An = As[(s0 + s) * CH + c], A2 = An * kLog2e, x0 = xin[s * CH], r0 = rin[s * CH];
+        const float4* Bp = reinterpret_cast<const float4*>(sm.tile[it & 1][0][s]) + tl;
+        const float4* Cp = reinterpret_cast<const float4*>(sm.tile[it & 1][1][s]) + tl;
+        const float4 b0 = Bp[0], b1 = Bp[TL], c0 = Cp[0], c1 = Cp[TL];
+        const float2 Bv[PAIRS] = {{b0.x, b0.y}, {b0.z, b0.w}, {b1.x, b1.y}, {b1.z, b1.w}};
+        const float2 Cv[PAIRS] = {{c0.x, c0.y}, {c0.z, c0.w}, {c1.x, c1.y}, {c1.z, c1.w}};
+        float2 a[PAIRS], w[PAIRS], cy[PAIRS], ax[PAIRS];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) a[i] = ex2(dt[i] * A2);
-        // forward: states from the kept one
-        const float P = ex2(sum * A2);
-        float hh = du[0] * Bv[0];
-#pragma unroll
-        for (int i = 1; i < 8; ++i) hh = fmaf(a[i], hh, du[i] * Bv[i]);
-        float x0 = 0.f;
-        if (tl == 0) {
-          x0 = live ? __ldg(q.ckpt + (row * nck + k) * N + s0 + s) : 0.f;
-          hh = fmaf(P, x0, hh);
+        for (int i = 0; i < PAIRS; ++i) {
+          const float2 e = mul2(dt[i], both(A2));
+          a[i] = make_float2(ex2(e.x), ex2(e.y));
+          w[i] = mul2(du[i], Bv[i]);
+          cy[i] = mul2(Cv[i], dyp[i]);
         }
-        float Pf = P;
+        // both recurrences from zero: hf is the state at the lane's end, hb what its first step hands on
+        float Pf = ex2(sum * A2), Pb = Pf;
+        float hf = fmaf(a[0].y, w[0].x, w[0].y);
 #pragma unroll
-        for (int d = 1; d < TL; d *= 2) {
-          const float hp = __shfl_up_sync(~0u, hh, d, TL), Pp = __shfl_up_sync(~0u, Pf, d, TL);
-          if (tl >= d) {
-            hh = fmaf(Pf, hp, hh);
-            Pf *= Pp;
-          }
+        for (int i = 1; i < PAIRS; ++i) {
+          hf = fmaf(a[i].x, hf, w[i].x);
+          hf = fmaf(a[i].y, hf, w[i].y);
         }
-        const float up = __shfl_up_sync(~0u, hh, 1, TL);
-        float x = tl == 0 ? x0 : up;
+        float2 ac = mul2(a[PAIRS - 1], cy[PAIRS - 1]);
+        float hb = fmaf(a[PAIRS - 1].x, ac.y, ac.x);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ax[i] = a[i] * x;
-          x = fmaf(du[i], Bv[i], ax[i]);
-          y0[i] = fmaf(Cv[i], x, y0[i]);
-          r[i] = dyp[i] * x;
+        for (int i = PAIRS - 2; i >= 0; --i) {
+          ac = mul2(a[i], cy[i]);
+          hb = fmaf(a[i].y, hb, ac.y);
+          hb = fmaf(a[i].x, hb, ac.x);
         }
-        const float2 dc = sum_channels(r, cl);
-        // backward: r = a g, what a step hands to the one before it
-        float rr = 0.f;
+        hf = fmaf(Pf, x0, hf);
+        hb = fmaf(Pb, r0, hb);
+        join<true, 1>(hf, Pf);
+        join<false, 1>(hb, Pb);
+        join<true, 2>(hf, Pf);
+        join<false, 2>(hb, Pb);
+        join<true, 4>(hf, Pf);
+        join<false, 4>(hb, Pb);
+        put_shared(r1s + (s0 + s) * CH * 4, hb);
+        float x = neighbour<true>(hf, x0), r = neighbour<false>(hb, r0);
+        float2 v[PAIRS];  // dC, then dB of the channel
 #pragma unroll
-        for (int i = 7; i >= 0; --i) rr = a[i] * fmaf(Cv[i], dyp[i], rr);
-        float r0 = 0.f;
-        if (tl == TL - 1) {
-          r0 = gs[(s0 + s) * CH + c];
-          rr = fmaf(P, r0, rr);
+        for (int i = 0; i < PAIRS; ++i) {
+          ax[i].x = a[i].x * x;
+          float2 xv;
+          xv.x = x = ax[i].x + w[i].x;
+          ax[i].y = a[i].y * x;
+          xv.y = x = ax[i].y + w[i].y;
+          y0[i] = fma2(Cv[i], xv, y0[i]);
+          v[i] = mul2(dyp[i], xv);
         }
-        float Pb = P;
+        float* out = sm.sums[warp][s][0] + tl * 8 + cl * 2;
+        *reinterpret_cast<float2*>(out + TB) = sum_channels(v, cl);
+        float2 da = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int d = 1; d < TL; d *= 2) {
-          const float rp = __shfl_down_sync(~0u, rr, d, TL), Pp = __shfl_down_sync(~0u, Pb, d, TL);
-          if (tl + d < TL) {
-            rr = fmaf(Pb, rp, rr);
-            Pb *= Pp;
-          }
+        for (int i = PAIRS - 1; i >= 0; --i) {
+          float2 gg;
+          gg.y = cy[i].y + r;
+          r = a[i].y * gg.y;
+          gg.x = cy[i].x + r;
+          r = a[i].x * gg.x;
+          gB[i] = fma2(gg, Bv[i], gB[i]);
+          const float2 mm = mul2(gg, ax[i]);
+          v[i] = mul2(gg, du[i]);
+          gA[i] = fma2(both(An), mm, gA[i]);
+          da = fma2(dt[i], mm, da);
         }
-        const float down = __shfl_down_sync(~0u, rr, 1, TL);
-        float gn = tl == TL - 1 ? r0 : down;
-        __syncwarp();
-        if (tl == 0) gs[(s0 + s) * CH + c] = rr;
-        float da = 0.f;
+        *reinterpret_cast<float2*>(out) = sum_channels(v, cl);
+        float d = da.x + da.y;
 #pragma unroll
-        for (int i = 7; i >= 0; --i) {
-          const float gg = fmaf(Cv[i], dyp[i], gn);
-          gn = a[i] * gg;
-          r[i] = gg * du[i];
-          gB[i] = fmaf(gg, Bv[i], gB[i]);
-          const float m = gg * ax[i];
-          gA[i] = fmaf(An, m, gA[i]);
-          da = fmaf(dt[i], m, da);
-        }
-        const float2 db = sum_channels(r, cl);
-#pragma unroll
-        for (int d = 1; d < TL; d *= 2) da += __shfl_xor_sync(~0u, da, d);
-        if (tl == 0) das[(s0 + s) * CH + c] += da;
-        float* w = wb + ((warp * kStates + s) * 2) * TB + tl * 8 + cl * 2;
-        *reinterpret_cast<float2*>(w) = db;
-        *reinterpret_cast<float2*>(w + TB) = dc;
+        for (int e = CL; e < 32; e *= 2) d += __shfl_xor_sync(~0u, d, e);
+        da_at[(s0 + s) * CH] += d;
       }
+      if (more) commit_tile(kn, cn, it + 1);
       __syncthreads();
       for (int i = tid; i < ns * 2 * TB; i += kThreads) {
+        const int t = k * TB + i % TB;
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += wb[w * kStates * 2 * TB + i];
-        const int t = tb + i % TB, s = s0 + i / (2 * TB), which = i / TB & 1;
-        if (t < p.L) pbc[which * pstep + (long long)s * p.L + t] = v;
+        for (int w = 0; w < kWarps; ++w) v += (&sm.sums[w][0][0][0])[i];
+        if (t < p.L) pbc[(i / TB & 1) * pstep + (long long)(s0 + i / (2 * TB)) * p.L + t] = v;
       }
+      __syncthreads();
     }
-    if (live) {
-      float v[8], o[8];
-      load8(u, t0, p.L, n, p.u.vec, v);
-      if (t0 < p.L) {
+    if (live && t0 < p.L) {
+      float v[8], o[8], w[8];
+      take8(sm.in[k & 1][0][tid], t0, n, v);
+      float sd = 0.f, sb = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = fmaf(dt[i], gB[i], Dh * dyp[i]);
-          sum_d = fmaf(dyp[i], v[i], sum_d);
-        }
-        store8((T*)q.du + row * p.L, t0, p.L, n, p.out_vec, o);
-        float raw[8];
-        load8(delta, t0, p.L, n, p.delta.vec, raw);
+      for (int i = 0; i < PAIRS; ++i) {
+        o[2 * i] = fmaf(dt[i].x, gB[i].x, Dh * dyp[i].x);
+        o[2 * i + 1] = fmaf(dt[i].y, gB[i].y, Dh * dyp[i].y);
+        sd = fmaf(dyp[i].x, v[2 * i], fmaf(dyp[i].y, v[2 * i + 1], sd));
+      }
+      sum_d += sd;
+      store8((T*)q.du + row * p.L, t0, p.L, n, p.out_vec, o);
+      take8(sm.in[k & 1][1][tid], t0, n, w);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[i] = fmaf(v[i], gB[i], gA[i]);
-          if (p.softplus) o[i] *= sigmoid(raw[i] + bias);
-          if (t0 + i < n) sum_bias += o[i];
-        }
-        store8((T*)q.ddelta + row * p.L, t0, p.L, n, p.out_vec, o);
-        if (z) {
-          float dyv[8];
-          load8(z, t0, p.L, n, p.z.vec, v);
-          load8(dy, t0, p.L, n, p.dy.vec, dyv);
+      for (int i = 0; i < PAIRS; ++i) {
+        o[2 * i] = fmaf(v[2 * i], gB[i].x, gA[i].x);
+        o[2 * i + 1] = fmaf(v[2 * i + 1], gB[i].y, gA[i].y);
+      }
 #pragma unroll
-          for (int i = 0; i < 8; ++i) o[i] = dyv[i] * y0[i] * dsilu(v[i]);
-          store8((T*)q.dz + row * p.L, t0, p.L, n, p.out_vec, o);
+      for (int i = 0; i < 8; ++i) {
+        if (p.softplus) o[i] *= sigmoid(w[i] + bias);
+        if (t0 + i < n) sb += o[i];
+      }
+      sum_bias += sb;
+      store8((T*)q.ddelta + row * p.L, t0, p.L, n, p.out_vec, o);
+      if (z) {
+        take8(sm.in[k & 1][2][tid], t0, n, v);
+        take8(sm.in[k & 1][3][tid], t0, n, w);
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+          o[2 * i] = v[2 * i] * y0[i].x * dsilu(w[2 * i]);
+          o[2 * i + 1] = v[2 * i + 1] * y0[i].y * dsilu(w[2 * i + 1]);
         }
+        store8((T*)q.dz + row * p.L, t0, p.L, n, p.out_vec, o);
       }
     }
   }
 #pragma unroll
-  for (int d = 1; d < TL; d *= 2) {
+  for (int d = CL; d < 32; d *= 2) {
     sum_d += __shfl_xor_sync(~0u, sum_d, d);
     sum_bias += __shfl_xor_sync(~0u, sum_bias, d);
   }
+  const long long part = (long long)b * sg.count + seg;
   if (live && tl == 0) {
-    q.part_d[row] = sum_d;
-    q.part_d[(long long)p.B * p.H + row] = sum_bias;
+    q.part_d[part * p.H + h] = sum_d;
+    q.part_d[((long long)p.B * sg.count + part) * p.H + h] = sum_bias;
   }
   __syncthreads();
   for (int i = tid; i < N * CH; i += kThreads) {
-    const int cc = i / N, s = i % N;
+    const int cc = i / N, s = i % N, hh = g * E + tile * CH + cc;
     if (tile * CH + cc >= E) continue;
-    const long long at = ((long long)b * p.H + g * E + tile * CH + cc) * N + s;
-    q.part_a[at] = das[s * CH + cc];
-    if (q.dstate_in) q.dstate_in[at] = gs[s * CH + cc];
+    q.part_a[(part * p.H + hh) * N + s] = das[s * CH + cc];
+    if (q.dstate_in && seg == 0) q.dstate_in[((long long)b * p.H + hh) * N + s] = gs[s * CH + cc];
   }
 }
 
@@ -317,33 +441,55 @@ __global__ void scan_sum_rows_kernel(const float* part_a, const float* part_d, f
   }
 }
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
-
 struct Plan {
   int tiles;
+  Segments sg;
   size_t bc, a, d;  // bytes of the parts
 };
 Plan plan(int B, int H, int L, int N, int G) {
-  const int tiles = (H / G + CH - 1) / CH;
-  return {tiles, up256((size_t)tiles * 2 * B * G * N * L * 4), up256((size_t)B * H * N * 4), up256((size_t)2 * B * H * 4)};
+  const int tiles = (H / G + CH - 1) / CH, all = (L + TB - 1) / TB, sms = num_sms();
+  const long long ctas = (long long)tiles * B * G;
+  Plan r{tiles, {1, all, nullptr, nullptr}, 0, 0, 0};
+  float least = -1.f;
+  for (int want = 1; want <= 64 && (want == 1 || ctas * (want - 1) < 16 * sms); ++want) {
+    const int blocks = (all + want - 1) / want, count = (all + blocks - 1) / blocks;
+    if (count != want || (count > 1 && blocks < 4)) continue;
+    // measured: 144 us and 89 us for each thread block on an SM, 2048 steps of 16 states in bf16
+    const float t = scan_cost(ctas * count, blocks, kMinBlocks, 144.f, 89.f, sms) +
+                    (count > 1 ? ends_cost(B, H, G, N, count, blocks, sms) : 0.f);
+    if (least < 0.f || t < least) {
+      least = t;
+      r.sg = {count, blocks, nullptr, nullptr};
+    }
+  }
+  r.bc = up256((size_t)tiles * 2 * B * G * N * L * 4);
+  r.a = up256((size_t)B * r.sg.count * H * N * 4);
+  r.d = up256((size_t)2 * B * r.sg.count * H * 4);
+  return r;
 }
 
 template <typename T>
 cudaError_t bwd(const ScanArgs& p, BwdOut q, void* dB, void* dC, float* dA, float* dD, float* dbias, char* ws,
-                cudaStream_t st) {
-  const Plan pl = plan(p.B, p.H, p.L, p.N, p.G);
+                int dtype, cudaStream_t st) {
+  Plan pl = plan(p.B, p.H, p.L, p.N, p.G);
   q.part_bc = (float*)ws;
   q.part_a = (float*)(ws + pl.bc);
   q.part_d = (float*)(ws + pl.bc + pl.a);
-  const size_t smem = (size_t)(2 * kStates * TB + kWarps * kStates * 2 * TB + 3 * p.N * CH) * 4;
-  cudaError_t e = smem_optin<scan_bwd_kernel<T>>(smem);
+  place_segments(&pl.sg, ws + pl.bc + pl.a + pl.d, p.B, p.H, p.N);
+  cudaError_t e;
+  if (pl.sg.count > 1 && (e = launch_segment_states(p, pl.sg, q.dstate_out, true, dtype, st)) != cudaSuccess) return e;
+  const int Np = (p.N + kStates - 1) / kStates * kStates;
+  const size_t smem = sizeof(Sm<T>) + (size_t)5 * Np * CH * 4;
+  e = smem_optin<scan_bwd_kernel<T>>(smem);
   if (e != cudaSuccess) return e;
-  scan_bwd_kernel<T><<<(unsigned)((long long)pl.tiles * p.B * p.G), kThreads, smem, st>>>(p, q, pl.tiles);
+  scan_bwd_kernel<T><<<(unsigned)((long long)pl.tiles * p.B * p.G * pl.sg.count), kThreads, smem, st>>>(p, q, pl.sg,
+                                                                                                      pl.tiles);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const long long m = (long long)p.B * p.G * p.N * p.L, r = (long long)p.H * (p.N + 2);
   scan_sum_bc_kernel<T><<<(unsigned)((2 * m + 255) / 256), 256, 0, st>>>(q.part_bc, (T*)dB, (T*)dC, m, pl.tiles);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  scan_sum_rows_kernel<<<(unsigned)((r + 255) / 256), 256, 0, st>>>(q.part_a, q.part_d, dA, dD, dbias, p.B, p.H, p.N);
+  scan_sum_rows_kernel<<<(unsigned)((r + 255) / 256), 256, 0, st>>>(q.part_a, q.part_d, dA, dD, dbias,
+                                                                    p.B * pl.sg.count, p.H, p.N);
   return cudaGetLastError();
 }
 
@@ -351,7 +497,7 @@ cudaError_t bwd(const ScanArgs& p, BwdOut q, void* dB, void* dC, float* dA, floa
 
 size_t selective_scan_bwd_workspace_bytes(int B, int H, int L, int N, int G) {
   const Plan pl = plan(B, H, L, N, G);
-  return pl.bc + pl.a + pl.d;
+  return pl.bc + pl.a + pl.d + segments_bytes(pl.sg, B, H, N);
 }
 
 cudaError_t launch_selective_scan_bwd(const ScanArgs& p, const float* ckpt, void* du, void* ddelta, float* dA, void* dB,
@@ -359,9 +505,9 @@ cudaError_t launch_selective_scan_bwd(const ScanArgs& p, const float* ckpt, void
                                       float* dstate_in, void* workspace, int dtype, cudaStream_t st) {
   const BwdOut q{du, ddelta, dz, ckpt, dstate_out, dstate_in, nullptr, nullptr, nullptr};
   switch (dtype) {
-    case 0: return bwd<float>(p, q, dB, dC, dA, dD, ddt_bias, (char*)workspace, st);
-    case 1: return bwd<__half>(p, q, dB, dC, dA, dD, ddt_bias, (char*)workspace, st);
-    case 2: return bwd<__nv_bfloat16>(p, q, dB, dC, dA, dD, ddt_bias, (char*)workspace, st);
+    case 0: return bwd<float>(p, q, dB, dC, dA, dD, ddt_bias, (char*)workspace, dtype, st);
+    case 1: return bwd<__half>(p, q, dB, dC, dA, dD, ddt_bias, (char*)workspace, dtype, st);
+    case 2: return bwd<__nv_bfloat16>(p, q, dB, dC, dA, dD, ddt_bias, (char*)workspace, dtype, st);
     default: return cudaErrorInvalidValue;
   }
 }
