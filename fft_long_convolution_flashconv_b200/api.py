@@ -8,6 +8,7 @@ complex64 tensors.  I/O tensors are float32, float16 or bfloat16 CUDA tensors.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional
 
 import torch
@@ -296,40 +297,42 @@ def _device(first: torch.Tensor, *others) -> torch.device:
 
 
 class _Call:
-    """Makes `device` current for a call where it is not."""
+    """Makes `device` current for a call where it is not, and gives its current
+    stream's handle."""
 
     def __init__(self, device: torch.device):
-        self.other = device.index != torch.cuda.current_device()
-        if self.other:
-            self.guard = torch.cuda.device(device)
+        self.index = device.index
+        self.guard = None if self.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
 
     def __enter__(self):
-        if self.other:
+        if self.guard is not None:
             self.guard.__enter__()
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
-        if self.other:
+        if self.guard is not None:
             self.guard.__exit__(*exc)
 
 
-def _check(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype) -> Optional[torch.Tensor]:
+def _check(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype) -> Optional[torch.Tensor]:
     if t is not None:
-        if t.dtype != dtype:
+        if t.dtype is not dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != tuple(shape):
+        if t.shape != shape:
             raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
 
-def _dense(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
+def _dense(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype):
     """A contiguous tensor of this shape and type, or None."""
+    if t is None:
+        return None
     if _check(t, name, shape, dtype) is not None and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return t
 
 
-def _seq(t: Optional[torch.Tensor], name: str, shape, dtype: torch.dtype):
+def _seq(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype):
     """A sequence of this shape and type with contiguous time, or None."""
     if _check(t, name, shape, dtype) is not None and shape[-1] > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
@@ -340,7 +343,9 @@ def _addr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+@functools.lru_cache(maxsize=256)
 def _strides(*values):
+    """The host array of these strides (only read by the library)."""
     return (ctypes.c_longlong * len(values))(*values)
 
 
@@ -362,7 +367,7 @@ def _lengths(lengths: Optional[torch.Tensor], B: int):
 
 
 def _sizes(t: torch.Tensor, name: str, dims: str):
-    if t.dim() != len(dims.split(" x ")):
+    if t.dim() != dims.count(" x ") + 1:
         raise ValueError(f"{name} must be {dims}, got shape {tuple(t.shape)}")
     if t.dtype not in _DT:
         raise ValueError(f"unsupported dtype {t.dtype}")
@@ -501,10 +506,10 @@ def selective_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bt
     ckpt = None
     if return_ckpt:
         ckpt = torch.empty(int(lib.selective_scan_ckpt_bytes(B, H, L, N)) // 4, dtype=torch.float32, device=dev)
-    need = int(lib.selective_scan_workspace(B, H, L, N, G))
-    if need or workspace is not None:
-        workspace = _need(workspace, need, dev)
     with _Call(dev) as st:
+        need = int(lib.selective_scan_workspace(B, H, L, N, G))
+        if need or workspace is not None:
+            workspace = _need(workspace, need, dev)
         check(lib.selective_scan_fwd(_addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D), _addr(dt_bias),
                                      _addr(z), _addr(out), B, H, L, N, G, bool(softplus), _addr(lengths),
                                      _strides(*strides), _addr(state_in), _addr(state), _addr(ckpt), _addr(workspace),
@@ -540,7 +545,6 @@ def selective_scan_bwd(dy: torch.Tensor, u: torch.Tensor, delta: torch.Tensor, A
     _dense(dstate_out, "dstate_out", (B, H, N), torch.float32)
     _lengths(lengths, B)
     dev = _device(u, dy, delta, A, Bt, Ct, ckpt, D, dt_bias, z, lengths, dstate_out)
-    workspace = _need(workspace, int(lib.selective_scan_bwd_workspace(B, H, L, N, G)), dev)
 
     def new(*shape, dtype=torch.float32, when=True):
         return torch.empty(shape, dtype=dtype, device=dev) if when else None
@@ -550,6 +554,7 @@ def selective_scan_bwd(dy: torch.Tensor, u: torch.Tensor, delta: torch.Tensor, A
     dD, dbias = new(H, when=D is not None), new(H, when=dt_bias is not None)
     dstate = new(B, H, N, when=need_dstate_in)
     with _Call(dev) as st:
+        workspace = _need(workspace, int(lib.selective_scan_bwd_workspace(B, H, L, N, G)), dev)
         check(lib.selective_scan_bwd(_addr(dy), _addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D),
                                      _addr(dt_bias), _addr(z), _addr(ckpt), _addr(du), _addr(ddelta), _addr(dA),
                                      _addr(dB), _addr(dC), _addr(dD), _addr(dbias), _addr(dz), B, H, L, N, G,
@@ -628,12 +633,12 @@ def group_norm_act_bwd(dy: torch.Tensor, x: torch.Tensor, groups: int, weight: O
     _dense(dy, "dy", (B, L, C), x.dtype)
     dev = _device(x, dy, weight, bias, gate)
     lib = _lib.load()
-    workspace = _need(workspace, int(lib.group_norm_act_bwd_workspace(B, L, C, groups, bool(channel_major))), dev)
     dx = torch.empty_like(x)
     dgate = torch.empty_like(gate) if gate is not None else None
     dw = torch.empty((C,), dtype=torch.float32, device=dev) if weight is not None else None
     db = torch.empty((C,), dtype=torch.float32, device=dev) if bias is not None else None
     with _Call(dev) as st:
+        workspace = _need(workspace, int(lib.group_norm_act_bwd_workspace(B, L, C, groups, bool(channel_major))), dev)
         check(lib.group_norm_act_bwd(_addr(dy), _addr(x), _addr(weight), _addr(bias), _addr(gate), _addr(dx), _addr(dw),
                                      _addr(db), _addr(dgate), B, L, C, groups, eps, bool(channel_major),
                                      _addr(workspace), workspace.numel() * workspace.element_size(), _DT[x.dtype], st),

@@ -797,7 +797,7 @@ FC_API fc_status group_norm_act_fwd(const void* x, const float* weight, const fl
 
 FC_API size_t group_norm_act_bwd_workspace(int B, int L, int C, int G, int channel_major) {
   if (B < 1 || L < 1 || C < 1 || G < 1 || C % G || C / G > 8192) return 0;
-  return (size_t)fc::group_norm_bwd_splits(B, L, C, G, channel_major) * 2 * C * 4;
+  return fc::group_norm_bwd_workspace_bytes(B, L, C, G, channel_major);
 }
 
 FC_API fc_status group_norm_act_bwd(const void* dy, const void* x, const float* weight, const float* bias,

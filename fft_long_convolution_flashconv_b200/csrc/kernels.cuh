@@ -141,10 +141,10 @@ cudaError_t launch_selective_scan_bwd(const ScanArgs& p, const float* ckpt, void
                                       float* dstate_in, void* workspace, int dtype, cudaStream_t st);
 
 // Group norm of each token with SiLU (group_norm.cu).  vec: rows and groups
-// start on 16-byte boundaries.  part: float scratch of group_norm_bwd_splits() * 2 C.
+// start on 16-byte boundaries.  part: scratch of group_norm_bwd_workspace_bytes().
 cudaError_t launch_group_norm(const void* x, const float* w, const float* bias, const void* gate, void* y, int B, int L,
                               int C, int G, float eps, int channel_major, int vec, int dtype, cudaStream_t st);
-int group_norm_bwd_splits(int B, int L, int C, int G, int channel_major);
+size_t group_norm_bwd_workspace_bytes(int B, int L, int C, int G, int channel_major);
 cudaError_t launch_group_norm_bwd(const void* dy, const void* x, const float* w, const float* bias, const void* gate,
                                   void* dx, float* dw, float* dbias, void* dgate, int B, int L, int C, int G, float eps,
                                   int channel_major, int vec, float* part, int dtype, cudaStream_t st);

@@ -10,6 +10,10 @@ namespace fc {
 
 constexpr int kVec = 8;  // time steps per thread and load
 
+// Guarded element loads here are plain ones: the headers' __ldg of a 16-bit type
+// is an assembly statement without side effects, which the compiler may move out
+// of its condition (a null or out-of-range address is then read).
+
 // A B x H x L (or B x G x N x L) tensor with contiguous time: element strides of
 // a batch, of a row and of a group; vec = every row starts on a 16-byte boundary.
 struct Rows {
@@ -96,7 +100,7 @@ __device__ __forceinline__ void load8(const T* row, long long t0, int L, int n, 
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = t0 + i < n ? IO<T>::ld(row + t0 + i) : 0.f;
+    for (int i = 0; i < 8; ++i) v[i] = t0 + i < n ? IO<T>::ldplain(row + t0 + i) : 0.f;
   }
 }
 
@@ -147,14 +151,44 @@ __device__ __forceinline__ int row_length(const int* lengths, int b, int L) {
   return lengths ? min(max(__ldg(lengths + b), 0), L) : L;
 }
 
-// Sigmoid and SiLU x s(x).  exp(-x) = infinity for x < -88 gives s = 0.
-__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+// 2^x and 1 / x by the special function unit (relative errors of 2^-22 and 2^-23;
+// results below 2^-126 are zero).
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+constexpr float kLog2e = 1.4426950408889634f;
+
+// Two sums or products at once (fp32 pairs of neighbouring registers).
+__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+
+// Sigmoid, SiLU x s(x) and its derivative.  exp(-x) = infinity for x < -88 gives s = 0.
+__device__ __forceinline__ float2 sigmoid2(float2 x) {
+  const float2 e = mul2(x, both(-kLog2e));
+  const float2 d = add2(make_float2(ex2(e.x), ex2(e.y)), both(1.f));
+  return make_float2(rcp(d.x), rcp(d.y));
+}
+__device__ __forceinline__ float2 silu2(float2 x) { return mul2(x, sigmoid2(x)); }
+__device__ __forceinline__ float2 dsilu2(float2 x) {
+  const float2 s = sigmoid2(x);  // s (1 + x (1 - s))
+  return mul2(s, fma2(x, fma2(s, both(-1.f), both(1.f)), both(1.f)));
+}
+__device__ __forceinline__ float sigmoid(float x) { return rcp(1.f + ex2(x * -kLog2e)); }
 __device__ __forceinline__ float silu(float x) { return x * sigmoid(x); }
-// Derivative of SiLU.
 __device__ __forceinline__ float dsilu(float x) {
   const float s = sigmoid(x);
   return s * fmaf(x, 1.f - s, 1.f);
 }
+__device__ __forceinline__ float2 pair(const float (&v)[8], int i) { return make_float2(v[2 * i], v[2 * i + 1]); }
 
 // Row b of a decode batch: its place in the state pool, or -1 for a padded row
 // (a slot outside [0, S), or one that an earlier row of the batch holds).

@@ -20,20 +20,6 @@ struct ScanArgs {
   int softplus, out_vec;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// Two products or sums at once (fp32 pairs of neighbouring registers).
-__device__ __forceinline__ float2 mul2(float2 a, float2 b) { return __fmul2_rn(a, b); }
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
-__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) { return __fadd2_rn(a, b); }
-
-constexpr float kLog2e = 1.4426950408889634f;
-
 // log(1 + exp(x)) = max(x, 0) + log(1 + e), e = exp(-|x|).  log(1 + e) = e q(e)
 // with q a degree-9 Chebyshev interpolant on [0, 1] (relative error below
 // 1.2e-7 in fp32), so small step sizes keep their relative precision without a

@@ -337,64 +337,102 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, 
   }
 }
 
-// One token.  LPC lanes share a channel, each four states at a time (one
-// 16-byte access where N is a multiple of four).
-template <typename T>
-__global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs p, float* state, T* y, const int* slots, int S,
-                                                             int lpc, int vec) {
-  const int b = blockIdx.y, sub = threadIdx.x % lpc;
-  const int h = blockIdx.x * (kThreads / lpc) + threadIdx.x / lpc;
-  const int slot = batch_slot(slots, b, S);
-  const bool live = h < p.H;
-  const int hh = live ? h : 0, N = p.N, g = hh / (p.H / p.G);
-  if (slot < 0) {
-    if (live && sub == 0) IO<T>::st(y + (long long)b * p.H + h, 0.f);
-    return;
+// One token.  LPC lanes share a channel, four states (one 16-byte access where N
+// is a multiple of four) of each; a thread takes kTok channels, whose states it
+// loads before anything is known of the slot but its range, and B and C once for
+// all.  Lane j % LPC of a channel's lanes computes the step size and the gate of
+// its j-th channel for the others.
+constexpr int kTok = 4;
+
+template <typename T, bool VEC, int LPC>
+__global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs p, float* state, T* y, const int* slots, int S) {
+  constexpr int per = kThreads / LPC, own = (kTok + LPC - 1) / LPC;  // channels apart; those a lane answers for
+  const int b = blockIdx.y, sub = threadIdx.x % LPC, N = p.N;
+  const int h0 = blockIdx.x * per * kTok + threadIdx.x / LPC;  // channels h0, h0 + per, ...
+  const int raw = slots ? __ldg(slots + b) : b;
+  float* const pool = state + (raw >= 0 && raw < S ? (long long)raw * p.H * N : 0);
+  const int s = sub * 4;
+  float4 x[kTok], A[kTok];
+  auto load4 = [&](const float* q, int at) {
+    if (VEC) return at < N ? *reinterpret_cast<const float4*>(q + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    return make_float4(at < N ? q[at] : 0.f, at + 1 < N ? q[at + 1] : 0.f, at + 2 < N ? q[at + 2] : 0.f,
+                       at + 3 < N ? q[at + 3] : 0.f);
+  };
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {  // channels behind the last read the last one's
+    const long long at = (long long)min(h0 + j * per, p.H - 1) * N;
+    x[j] = load4(pool + at, s);
+    A[j] = load4(p.A + at, s);
   }
-  const float u = IO<T>::ld((const T*)p.u.p + b * p.u.bs + hh * p.u.rs);
-  float dt = IO<T>::ld((const T*)p.delta.p + b * p.delta.bs + hh * p.delta.rs);
-  if (p.dt_bias) dt += __ldg(p.dt_bias + hh);
-  if (p.softplus) dt = softplus(dt);
-  const float du = dt * u;
-  const T* Bt = (const T*)p.Bt.p + b * p.Bt.bs + g * p.Bt.gs;
-  const T* Ct = (const T*)p.Ct.p + b * p.Ct.bs + g * p.Ct.gs;
-  float* xp = state + ((long long)slot * p.H + hh) * N;
-  const float* Ap = p.A + (long long)hh * N;
-  float acc = 0.f;
-  for (int s = sub * 4; s < N; s += lpc * 4) {
-    float x[4], A[4];
-    if (vec) {
-      const float4 xv = *reinterpret_cast<const float4*>(xp + s), av = __ldg(reinterpret_cast<const float4*>(Ap + s));
-      x[0] = xv.x; x[1] = xv.y; x[2] = xv.z; x[3] = xv.w;
-      A[0] = av.x; A[1] = av.y; A[2] = av.z; A[3] = av.w;
-    } else {
+  // step size, u and gate of the channels that this lane answers for: j = e LPC + sub
+  float dt[own], u[own], z[own];
+#pragma unroll
+  for (int e = 0; e < own; ++e) {
+    const int h = min(h0 + (e * LPC + sub) % kTok * per, p.H - 1);
+    u[e] = IO<T>::ldplain((const T*)p.u.p + b * p.u.bs + h * p.u.rs);
+    dt[e] = IO<T>::ldplain((const T*)p.delta.p + b * p.delta.bs + h * p.delta.rs);
+    if (p.dt_bias) dt[e] += __ldg(p.dt_bias + h);
+    z[e] = p.z.p ? IO<T>::ldplain((const T*)p.z.p + b * p.z.bs + h * p.z.rs) : 0.f;
+  }
+  float Bv[4], Cv[4];
+  int group = -1;
+  const int slot = batch_slot(slots, b, S);
+#pragma unroll
+  for (int e = 0; e < own; ++e) {
+    if (p.softplus) dt[e] = softplus(dt[e]);
+    z[e] = p.z.p ? silu(z[e]) : 1.f;
+  }
+#pragma unroll
+  for (int j = 0; j < kTok; ++j) {
+    const int h = h0 + j * per;
+    const float d = __shfl_sync(~0u, dt[j / LPC], j % LPC, LPC), uj = __shfl_sync(~0u, u[j / LPC], j % LPC, LPC);
+    const float du = d * uj, d2 = d * kLog2e;
+    const int g = p.G == 1 ? 0 : min(h, p.H - 1) / (p.H / p.G);
+    const T* Bt = (const T*)p.Bt.p + b * p.Bt.bs + g * p.Bt.gs;
+    const T* Ct = (const T*)p.Ct.p + b * p.Ct.bs + g * p.Ct.gs;
+    if (g != group) {  // the lane's first four states
+      group = g;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        x[i] = s + i < N ? xp[s + i] : 0.f;
-        A[i] = s + i < N ? __ldg(Ap + s + i) : 0.f;
+        Bv[i] = s + i < N ? IO<T>::ldplain(Bt + (s + i) * p.Bt.rs) : 0.f;
+        Cv[i] = s + i < N ? IO<T>::ldplain(Ct + (s + i) * p.Ct.rs) : 0.f;
       }
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (s + i >= N) break;
-      x[i] = fmaf(ex2(dt * A[i] * kLog2e), x[i], du * IO<T>::ld(Bt + (s + i) * p.Bt.rs));
-      acc = fmaf(IO<T>::ld(Ct + (s + i) * p.Ct.rs), x[i], acc);
-    }
-    if (live) {
-      if (vec) {
-        *reinterpret_cast<float4*>(xp + s) = make_float4(x[0], x[1], x[2], x[3]);
+    const bool on = h < p.H && slot >= 0;
+    float* const xp = pool + (long long)h * N;
+    float acc = 0.f;
+    auto update = [&](int q, float4 xv, float4 av, const float (&bv)[4], const float (&cv)[4]) {
+      xv = make_float4(fmaf(ex2(d2 * av.x), xv.x, du * bv[0]), fmaf(ex2(d2 * av.y), xv.y, du * bv[1]),
+                       fmaf(ex2(d2 * av.z), xv.z, du * bv[2]), fmaf(ex2(d2 * av.w), xv.w, du * bv[3]));
+      acc = fmaf(cv[0], xv.x, fmaf(cv[1], xv.y, fmaf(cv[2], xv.z, fmaf(cv[3], xv.w, acc))));
+      if (!on || q >= N) return;
+      if (VEC) {
+        *reinterpret_cast<float4*>(xp + q) = xv;
       } else {
+        xp[q] = xv.x;
+        if (q + 1 < N) xp[q + 1] = xv.y;
+        if (q + 2 < N) xp[q + 2] = xv.z;
+        if (q + 3 < N) xp[q + 3] = xv.w;
+      }
+    };
+    update(s, x[j], A[j], Bv, Cv);
+    if (LPC == 32 && on) {  // more than 128 states
+      for (int q = s + 4 * LPC; q < N; q += 4 * LPC) {
+        float bv[4], cv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (s + i < N) xp[s + i] = x[i];
+        for (int i = 0; i < 4; ++i) {
+          bv[i] = q + i < N ? IO<T>::ldplain(Bt + (q + i) * p.Bt.rs) : 0.f;
+          cv[i] = q + i < N ? IO<T>::ldplain(Ct + (q + i) * p.Ct.rs) : 0.f;
+        }
+        update(q, load4(xp, q), load4(p.A + (long long)h * N, q), bv, cv);
       }
     }
-  }
-  for (int d = lpc / 2; d; d >>= 1) acc += __shfl_xor_sync(~0u, acc, d);
-  if (live && sub == 0) {
-    acc = fmaf(p.D ? __ldg(p.D + hh) : 0.f, u, acc);
-    if (p.z.p) acc *= silu(IO<T>::ld((const T*)p.z.p + b * p.z.bs + hh * p.z.rs));
-    IO<T>::st(y + (long long)b * p.H + h, acc);
+#pragma unroll
+    for (int e = LPC / 2; e; e >>= 1) acc += __shfl_xor_sync(~0u, acc, e);
+    if (h < p.H && sub == j % LPC) {
+      const float o = fmaf(p.D ? __ldg(p.D + h) : 0.f, uj, acc) * z[j / LPC];
+      IO<T>::st(y + (long long)b * p.H + h, slot < 0 ? 0.f : o);
+    }
   }
 }
 
@@ -450,14 +488,26 @@ Plan plan(int B, int H, int L, int N, int G) {
   return best;
 }
 
-template <typename T>
-cudaError_t step(const ScanArgs& p, float* state, void* y, const int* slots, int S, cudaStream_t st) {
+template <typename T, bool VEC>
+cudaError_t step_v(const ScanArgs& p, float* state, void* y, const int* slots, int S, cudaStream_t st) {
   int lpc = 1;
   while (lpc < 32 && lpc * 4 < p.N) lpc *= 2;
-  const int per = kThreads / lpc;
-  const int vec = p.N % 4 == 0 && ((uintptr_t)state & 15) == 0 && ((uintptr_t)p.A & 15) == 0;
-  scan_step_kernel<T><<<dim3((p.H + per - 1) / per, p.B), kThreads, 0, st>>>(p, state, (T*)y, slots, S, lpc, vec);
+  const int per = kThreads / lpc * kTok;
+  const dim3 grid((p.H + per - 1) / per, p.B);
+  switch (lpc) {
+    case 1: scan_step_kernel<T, VEC, 1><<<grid, kThreads, 0, st>>>(p, state, (T*)y, slots, S); break;
+    case 2: scan_step_kernel<T, VEC, 2><<<grid, kThreads, 0, st>>>(p, state, (T*)y, slots, S); break;
+    case 4: scan_step_kernel<T, VEC, 4><<<grid, kThreads, 0, st>>>(p, state, (T*)y, slots, S); break;
+    case 8: scan_step_kernel<T, VEC, 8><<<grid, kThreads, 0, st>>>(p, state, (T*)y, slots, S); break;
+    case 16: scan_step_kernel<T, VEC, 16><<<grid, kThreads, 0, st>>>(p, state, (T*)y, slots, S); break;
+    default: scan_step_kernel<T, VEC, 32><<<grid, kThreads, 0, st>>>(p, state, (T*)y, slots, S); break;
+  }
   return cudaGetLastError();
+}
+template <typename T>
+cudaError_t step(const ScanArgs& p, float* state, void* y, const int* slots, int S, cudaStream_t st) {
+  const bool vec = p.N % 4 == 0 && ((uintptr_t)state & 15) == 0 && ((uintptr_t)p.A & 15) == 0;
+  return vec ? step_v<T, true>(p, state, y, slots, S, st) : step_v<T, false>(p, state, y, slots, S, st);
 }
 
 }  // namespace

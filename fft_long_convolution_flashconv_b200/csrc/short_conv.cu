@@ -29,56 +29,95 @@ struct ConvArgs {
 // x[t] for t < 0: the state entering the row.
 template <typename T, int K>
 __device__ __forceinline__ float past(const T* s, int t) {
-  return s ? IO<T>::ld(s + (K - 1) + t) : 0.f;
+  return s ? IO<T>::ldplain(s + (K - 1) + t) : 0.f;
 }
 
-// A thread computes eight outputs of a row: its own vector and the one before
-// it (from L1) hold every input it needs, K - 1 <= 7.
+// A thread computes kPer vectors of eight outputs of a row, a block's width apart.
+// A vector and the one before it (from L1) hold every input it needs, K - 1 <= 7;
+// all of a thread's loads are issued before the first is used.
+constexpr int kPer = 4;
+
 template <typename T, int K>
 __global__ __launch_bounds__(kThreads) void short_conv_kernel(ConvArgs p, T* y, T* state_out, int nvec, int tx_log,
-                                                              long long nblk_x) {
+                                                              unsigned nblk_x) {
   const int tx = threadIdx.x & ((1 << tx_log) - 1), ty = threadIdx.x >> tx_log;
-  const long long row = (long long)(blockIdx.x / nblk_x) * (kThreads >> tx_log) + ty;
-  const int vec = (int)(blockIdx.x % nblk_x << tx_log) + tx;
-  if (row >= (long long)p.B * p.H || vec >= nvec) return;
-  const int b = (int)(row / p.H), h = (int)(row % p.H);
+  const unsigned by = blockIdx.x / nblk_x, bx = blockIdx.x - by * nblk_x;
+  const unsigned row = by * (kThreads >> tx_log) + ty;
+  const int v0 = (int)(bx * kPer << tx_log) + tx;
+  if (row >= (unsigned)p.B * p.H || v0 >= nvec) return;
+  const unsigned b = row / p.H, h = row - b * p.H;
   const int n = row_length(p.lengths, b, p.L);
   const T* x = (const T*)p.x.p + b * p.x.bs + h * p.x.rs;
-  const T* s = p.state_in ? (const T*)p.state_in + row * (K - 1) : nullptr;
-  const int t0 = vec * 8;
-  float a[16];  // x[t0 - 8 .. t0 + 7]
-  {
-    float v[8];
-    if (t0 > 0) {
-      load8(x, t0 - 8, p.L, n, p.x.vec, v);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = i >= 9 - K ? past<T, K>(s, i - 8) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = v[i];
-    load8(x, t0, p.L, n, p.x.vec, v);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) a[8 + i] = v[i];
-  }
+  const T* s = p.state_in ? (const T*)p.state_in + (long long)row * (K - 1) : nullptr;
+  T* out = y + (long long)row * p.L;
   float w[K];
 #pragma unroll
   for (int j = 0; j < K; ++j) w[j] = __ldg(p.w + (long long)h * K + j);
   const float bias = p.bias ? __ldg(p.bias + h) : 0.f;
-  float o[8];
+  auto outputs = [&](int t0, const float (&a)[16]) {  // a: x[t0 - 8 .. t0 + 7]
+    float o[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float c = bias;
+    for (int i = 0; i < 4; ++i) {
+      float2 c = both(bias);
 #pragma unroll
-    for (int j = 0; j < K; ++j) c = fmaf(w[j], a[8 + i - j], c);
-    o[i] = p.silu ? silu(c) : c;
+      for (int j = 0; j < K; ++j) {
+        c.x = fmaf(w[j], a[8 + 2 * i - j], c.x);
+        c.y = fmaf(w[j], a[9 + 2 * i - j], c.y);
+      }
+      if (p.silu) c = silu2(c);
+      o[2 * i] = c.x;
+      o[2 * i + 1] = c.y;
+    }
+    store8(out, t0, p.L, n, p.out_vec, o);
+  };
+  auto before = [&](float (&v)[8]) {  // the inputs before the row
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = i >= 9 - K ? past<T, K>(s, i - 8) : 0.f;
+  };
+  const int last = v0 + ((kPer - 1) << tx_log);
+  if (p.x.vec && (last + 1) * 8 <= n) {  // whole vectors inside the row
+    Raw8<T> own[kPer], prev[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const T* q = x + (v0 + (j << tx_log)) * 8;
+      ldraw8(q, own[j]);
+      if (K > 1 && (j > 0 || v0 > 0)) ldraw8(q - 8, prev[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      float v[8], a[16];
+      if (K > 1) {
+        unpack8(prev[j], v);
+        if (j == 0 && v0 == 0) before(v);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = v[i];
+      unpack8(own[j], v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[8 + i] = v[i];
+      outputs((v0 + (j << tx_log)) * 8, a);
+    }
+  } else {
+    for (int vec = v0; vec <= last && vec < nvec; vec += 1 << tx_log) {
+      const int t0 = vec * 8;
+      float v[8], a[16];
+      if (t0 > 0)
+        load8(x, t0 - 8, p.L, n, p.x.vec, v);
+      else
+        before(v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[i] = v[i];
+      load8(x, t0, p.L, n, p.x.vec, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) a[8 + i] = v[i];
+      outputs(t0, a);
+    }
   }
-  store8(y + row * p.L, t0, p.L, n, p.out_vec, o);
-  if (state_out && vec == 0) {
+  if (state_out && v0 == 0) {
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
       const int t = n - (K - 1) + i;
-      IO<T>::st(state_out + row * (K - 1) + i, t >= 0 ? IO<T>::ld(x + t) : past<T, K>(s, t));
+      IO<T>::st(state_out + (long long)row * (K - 1) + i, t >= 0 ? IO<T>::ldplain(x + t) : past<T, K>(s, t));
     }
   }
 }
@@ -95,7 +134,7 @@ __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(ConvArgs p, T*
   const int h = blockIdx.x;
   const long long items = (long long)p.B * nvec;
   const long long lo = (long long)blockIdx.y * per_split;
-  const long long hi = lo + per_split < items ? lo + per_split : items;
+  const int count = (int)(lo + per_split < items ? per_split : items - lo);  // may be below 1
   float w[K], dw[K], db = 0.f;
 #pragma unroll
   for (int j = 0; j < K; ++j) {
@@ -103,8 +142,11 @@ __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(ConvArgs p, T*
     dw[j] = 0.f;
   }
   const float bias = p.bias ? __ldg(p.bias + h) : 0.f;
-  for (long long it = lo + threadIdx.x; it < hi; it += kThreads) {
-    const int b = (int)(it / nvec), vec = (int)(it % nvec), t0 = vec * 8;
+  // item lo + i of the channel: batch row b, vector vec
+  int b = (int)((lo + threadIdx.x) / nvec), vec = (int)((lo + threadIdx.x) % nvec);
+  const int db_step = kThreads / nvec, dv_step = kThreads % nvec;
+  for (int i0 = threadIdx.x; i0 < count; i0 += kThreads) {
+    const int t0 = vec * 8;
     const long long row = (long long)b * p.H + h;
     const int n = row_length(p.lengths, b, p.L);
     const T* x = (const T*)p.x.p + b * p.x.bs + h * p.x.rs;
@@ -140,28 +182,51 @@ __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(ConvArgs p, T*
         for (int i = 0; i < 8; ++i) a[16 + i] = dc[8 + i] = 0.f;
       }
     }
+    const bool inner = t0 + 7 + K <= n;  // everything below lies in the row
     if (p.silu) {
 #pragma unroll
-      for (int i = 0; i < 7 + K; ++i) {
-        float c = bias;
+      for (int i = 0; i < 8 + K; i += 2) {  // pairs; the last may be one too many
+        float2 c = both(bias);
 #pragma unroll
-        for (int j = 0; j < K; ++j) c = fmaf(w[j], a[8 + i - j], c);
-        dc[i] = t0 + i < n ? dc[i] * dsilu(c) : 0.f;
+        for (int j = 0; j < K; ++j) {
+          c.x = fmaf(w[j], a[8 + i - j], c.x);
+          if (i + 1 < 16) c.y = fmaf(w[j], a[9 + i - j], c.y);
+        }
+        c = dsilu2(c);
+        dc[i] *= c.x;
+        if (i + 1 < 16) dc[i + 1] *= c.y;
       }
+    }
+    if (!inner) {  // a zero gradient behind the row's end stays one whatever c was
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (t0 + i >= n) dc[i] = 0.f;
     }
     float o[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       float v = 0.f;
 #pragma unroll
-      for (int j = 0; j < K; ++j) {
-        v = fmaf(w[j], dc[i + j], v);
-        if (t0 + i < n) dw[j] = fmaf(dc[i], a[8 + i - j], dw[j]);
-      }
-      db += dc[i];
-      const int k = t0 + i - (n - (K - 1));  // this input's place in state_out
-      if (ds && k >= 0 && k < K - 1) v += IO<T>::ld(ds + k);
+      for (int j = 0; j < K; ++j) v = fmaf(w[j], dc[i + j], v);
       o[i] = v;
+    }
+    if (inner) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        db += dc[i];
+#pragma unroll
+        for (int j = 0; j < K; ++j) dw[j] = fmaf(dc[i], a[8 + i - j], dw[j]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int k = t0 + i - (n - (K - 1));  // this input's place in state_out
+        if (ds && k >= 0 && k < K - 1) o[i] += IO<T>::ldplain(ds + k);
+        if (t0 + i >= n) continue;
+        db += dc[i];
+#pragma unroll
+        for (int j = 0; j < K; ++j) dw[j] = fmaf(dc[i], a[8 + i - j], dw[j]);
+      }
     }
     store8(dx + row * p.L, t0, p.L, n, p.out_vec, o);
     if (dstate_in && vec == 0) {
@@ -174,9 +239,15 @@ __global__ __launch_bounds__(kThreads) void short_conv_bwd_kernel(ConvArgs p, T*
           if (t >= 0) v = fmaf(w[j], dc[t], v);
         }
         const int k = i - n;  // where the same input stands in state_out
-        if (ds && k >= 0) v += IO<T>::ld(ds + k);
+        if (ds && k >= 0) v += IO<T>::ldplain(ds + k);
         IO<T>::st(dstate_in + row * (K - 1) + i, v);
       }
+    }
+    b += db_step;
+    vec += dv_step;
+    if (vec >= nvec) {
+      vec -= nvec;
+      ++b;
     }
   }
   // sums over the block, in a fixed order
@@ -241,12 +312,13 @@ __global__ __launch_bounds__(kThreads) void short_conv_step_kernel(const T* x, l
 template <typename T, int K>
 cudaError_t fwd(const ConvArgs& p, void* y, void* state_out, cudaStream_t st) {
   const int nvec = (p.L + 7) / 8;
-  int tx_log = 0;  // threads along a row: rows shorter than a block share it
-  while ((1 << tx_log) < kThreads && (1 << tx_log) < nvec) ++tx_log;
-  const long long rows = (long long)p.B * p.H, rpb = kThreads >> tx_log;
-  const long long nblk_x = (nvec + (1LL << tx_log) - 1) >> tx_log;
+  int tx_log = 0;  // threads along a row: shorter rows share a block
+  while ((1 << tx_log) < kThreads && (kPer << tx_log) < nvec) ++tx_log;
+  const long long rows = (long long)p.B * p.H, rpb = kThreads >> tx_log, wide = (long long)kPer << tx_log;
+  const long long nblk_x = (nvec + wide - 1) / wide;
   const long long grid = (rows + rpb - 1) / rpb * nblk_x;
-  short_conv_kernel<T, K><<<(unsigned)grid, kThreads, 0, st>>>(p, (T*)y, (T*)state_out, nvec, tx_log, nblk_x);
+  short_conv_kernel<T, K><<<(unsigned)grid, kThreads, 0, st>>>(p, (T*)y, (T*)state_out, nvec, tx_log,
+                                                               (unsigned)nblk_x);
   return cudaGetLastError();
 }
 
