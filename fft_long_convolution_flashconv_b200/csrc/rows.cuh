@@ -129,6 +129,30 @@ __device__ __forceinline__ void stvec8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = o;
 }
 
+// Two neighbouring elements, and eight 16-bit ones from an address on a
+// two-byte boundary: as 4-byte words, with single elements at both ends where the
+// first is not on a 4-byte boundary.
+__device__ __forceinline__ void st2(float* p, float a, float b) { *reinterpret_cast<float2*>(p) = make_float2(a, b); }
+__device__ __forceinline__ void st2(__half* p, float a, float b) {
+  *reinterpret_cast<__half2*>(p) = __floats2half2_rn(a, b);
+}
+__device__ __forceinline__ void st2(__nv_bfloat16* p, float a, float b) {
+  *reinterpret_cast<__nv_bfloat162*>(p) = __floats2bfloat162_rn(a, b);
+}
+template <typename T>
+__device__ __forceinline__ void st8_any(T* p, const float (&v)[8]) {
+  if (reinterpret_cast<uintptr_t>(p) & 2) {
+    IO<T>::st(p, v[0]);
+    st2(p + 1, v[1], v[2]);
+    st2(p + 3, v[3], v[4]);
+    st2(p + 5, v[5], v[6]);
+    IO<T>::st(p + 7, v[7]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) st2(p + 2 * i, v[2 * i], v[2 * i + 1]);
+  }
+}
+
 // Store v at t0 .. t0 + 7 of an output row of length L (zeros at n and behind).
 template <typename T>
 __device__ __forceinline__ void store8(T* row, long long t0, int L, int n, bool vec, float (&v)[8]) {
@@ -139,11 +163,17 @@ __device__ __forceinline__ void store8(T* row, long long t0, int L, int n, bool 
   }
   if (vec && t0 + 8 <= L) {
     stvec8(row + t0, v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      if (t0 + i < L) IO<T>::st(row + t0 + i, v[i]);
+    return;
   }
+  if constexpr (sizeof(T) == 2) {
+    if (t0 + 8 <= L) {
+      st8_any(row + t0, v);
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (t0 + i < L) IO<T>::st(row + t0 + i, v[i]);
 }
 
 // lengths[b] clamped to [0, L]; L without lengths.
