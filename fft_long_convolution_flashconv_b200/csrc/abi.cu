@@ -623,7 +623,7 @@ static fc_status scan_args(fc::ScanArgs* p, const void* u, const void* delta, co
   FC_REQUIRE(N >= 1 && G >= 1, FC_EINVAL, "N, G must be >= 1 (got %d, %d)", N, G);
   FC_REQUIRE(N <= 256, FC_EUNSUPPORTED, "N = %d > 256", N);
   FC_REQUIRE(H % G == 0, FC_EINVAL, "H = %d is not a multiple of G = %d", H, G);
-  FC_REQUIRE((double)B * G * N * L < 274877906944.0, FC_EUNSUPPORTED, "B * G * N * L must be below 2^38");
+  FC_REQUIRE((double)B * G * N * L < 137438953472.0, FC_EUNSUPPORTED, "B * G * N * L must be below 2^37");
   FC_REQUIRE(u && delta && A && Bt && Ct, FC_EINVAL, "null u, delta, A, Bt or Ct");
   const size_t e = dtype_size(dtype);
   FC_REQUIRE(aligned(u, e) && aligned(delta, e) && aligned(z, e) && aligned(Bt, e) && aligned(Ct, e) &&

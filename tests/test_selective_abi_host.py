@@ -107,7 +107,7 @@ def scan_step(**kw):
     (dict(y=P2), EINVAL, "overlap"), (dict(y=P4), EINVAL, "overlap"), (dict(z=P5), EINVAL, "overlap"),
     (dict(ckpt=P5), EINVAL, "ckpt"), (dict(sin=P6, sout=P6), EINVAL, "state_out"), (dict(dtype=-1), EINVAL, "dtype"),
     (dict(strides=_ll(*[240, 40] * 3, 640, -320, 40, 640, 320, 40)), EINVAL, "strides"),
-    (dict(L=1 << 30, B=1, H=256, N=256, G=256), EUNSUP, "2^38"),
+    (dict(L=1 << 30, B=1, H=256, N=256, G=256), EUNSUP, "2^37"),
 ])
 def test_selective_scan_fwd_refusals(bad, status, word):
     assert scan_fwd(**bad) == status

@@ -682,3 +682,145 @@ def test_offsets_past_31_bits():
     w = one[0, 0].double()
     assert bool(((s[1, H - 1].double() - w).abs() <= 2 * 2.0 ** -11 * w.abs() * (1 + kappa(128)) + kappa(128) * 10).all())
     assert float((state[1, H - 1] - ostate[0, 0]).abs().max()) <= kappa(128) * 10
+
+
+# ------------------------------------------------------------------ long rows, other callers' ways
+@pytest.mark.parametrize("B,H,L,N,G,dtype", [(3, 5, 1000, 16, 1, "f32"), (2, 34, 777, 20, 2, "f16"),
+                                             (1, 1, 1500, 3, 1, "bf16")])
+def test_scan_in_segments(B, H, L, N, G, dtype):
+    """Few channels and many steps: rows are cut into segments; lengths end in the first, a middle and the last one."""
+    assert api.selective_scan_workspace_bytes(B, H, L, N, G) > 0
+    c = scan_case(B, H, L, N, G, dtype, 77, ("D", "bias", "gate", "state", "ragged"))
+    if B == 3:
+        c["n"] = torch.tensor([L, 70, 530], dtype=torch.int32)
+    # decays down to e^-1 over the whole row, so that segments matter to one another
+    c["dt_bias"] = torch.full((H,), -7.0)
+    want, mag = scan_want(c)
+    p = poison(c)
+    args, (y, state, ckpt) = call_fwd(p, return_state=True, return_ckpt=True)
+    close(y, want["y"], mag["y"], kappa(L), "y")
+    close(state, want["state"], mag["state"], kappa(L), "state")
+    got = api.selective_scan_bwd(p["dy"].cuda(), args["u"], args["delta"], c["A"].cuda(), args["Bt"], args["Ct"], ckpt,
+                                 cu(c["D"]), cu(c["dt_bias"]), args["z"], True, cu(c["n"]), cu(c["dso"]),
+                                 need_dstate_in=True)
+    for k, g in zip(("du", "ddelta", "dA", "dB", "dC", "dD", "ddt_bias", "dz", "dstate_in"), got):
+        close(g, want[k], mag[k], kappa(L, True), k)
+
+
+def test_scan_extreme_step_sizes_and_gates():
+    """Step sizes from e^-30 to 30 (a decays to nothing, or not at all), gates of +-100."""
+    c = scan_case(2, 8, 90, 8, 1, "f32", 21, ("D", "gate", "state"))
+    rng = np.random.default_rng(8)
+    c["delta"] = torch.tensor(rng.uniform(-30, 30, (2, 8, 90)), dtype=torch.float32)
+    c["z"] = torch.tensor(rng.choice([-100.0, -20.0, 0.0, 20.0, 100.0], (2, 8, 90)), dtype=torch.float32)
+    want, mag = scan_want(c)
+    args, (y, state, ckpt) = call_fwd(c, return_state=True, return_ckpt=True)
+    # a's argument |dt A| goes up to 30 * 11: where a is above 2^-126 its relative error is below 88 * 2^-21 a step,
+    # and only one such step can be in a term that is above e^-88; exp(-x) for a gate of -100 is zero or below 2^-126
+    k = kappa(90) + 2 * 88 * 2.0 ** -21
+    close(y, want["y"], mag["y"] + 2.0 ** -100, k, "y")
+    close(state, want["state"], mag["state"], k, "state")
+    got = api.selective_scan_bwd(c["dy"].cuda(), args["u"], args["delta"], c["A"].cuda(), args["Bt"], args["Ct"], ckpt,
+                                 cu(c["D"]), None, args["z"], dstate_out=cu(c["dso"]), need_dstate_in=True)
+    for name, g in zip(("du", "ddelta", "dA", "dB", "dC", "dD", None, "dz", "dstate_in"), got):
+        if name:
+            # silu' of +-100 is 1 or below e^-99 * 100: its own error is covered by an absolute 2^-100
+            close(g, want[name], mag[name] + 2.0 ** -100, 2 * k, name)
+
+
+def test_expanded_inputs_given_outputs_and_workspaces():
+    c = scan_case(3, 12, 700, 8, 1, "f16", 5, ("D", "bias", "gate"))
+    one = {k: c[k].cuda() for k in ("u", "delta", "A", "Bt", "Ct", "D", "dt_bias", "z")}
+    args = (one["u"], one["delta"], one["A"], one["Bt"][:1].expand(3, 1, 8, 700), one["Ct"][:1].expand(3, 1, 8, 700),
+            one["D"], one["dt_bias"], one["z"])
+    dense = [a.contiguous() for a in args]
+    want = api.selective_scan_fwd(*dense)
+    out = torch.full_like(want, NAN)
+    need = api.selective_scan_workspace_bytes(3, 12, 700, 8, 1)
+    ws = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    y = api.selective_scan_fwd(*args, workspace=ws, out=out)
+    assert y.data_ptr() == out.data_ptr() and torch.equal(y, want)
+    if need:
+        with pytest.raises(Exception, match="workspace too small"):
+            api.selective_scan_fwd(*args, workspace=ws[:need - 1].clone())
+    with pytest.raises(ValueError, match="out"):
+        api.selective_scan_fwd(*args, out=out[:, :, :-1])
+    with pytest.raises(Exception, match="16-byte"):
+        api.selective_scan_fwd(*args, out=torch.empty(want.numel() + 1, dtype=want.dtype, device="cuda")[1:].view_as(want))
+    x = one["u"][:, :1].expand(3, 12, 700)  # one channel for all, by stride
+    w = torch.randn(12, 4, device="cuda")
+    assert torch.equal(api.short_conv_fwd(x, w), api.short_conv_fwd(x.contiguous(), w))
+    dy = torch.randn(3, 12, 1, device="cuda").half().expand(3, 12, 700)
+    with pytest.raises(ValueError, match="last axis"):
+        api.short_conv_bwd(dy, x, w)
+    bw = torch.empty(api.short_conv_bwd_workspace_bytes(3, 12, 700, 4), dtype=torch.uint8, device="cuda")
+    a = api.short_conv_bwd(dy.contiguous(), x, w, workspace=bw)
+    b = api.short_conv_bwd(dy.contiguous(), x.contiguous(), w)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_a_batch_of_padding_touches_nothing():
+    B, H, N, S = 5, 20, 16, 3
+    slots = torch.full((B,), -1, dtype=torch.int32, device="cuda")
+    u = torch.full((B, H), NAN, device="cuda")
+    Bt = torch.full((B, 1, N), NAN, device="cuda")
+    A, w = -torch.ones(H, N, device="cuda"), torch.ones(H, 4, device="cuda")
+    state, ring = torch.randn(S, H, N, device="cuda"), torch.randn(S, H, 3, device="cuda")
+    s0, r0 = state.clone(), ring.clone()
+    assert not bool(api.selective_scan_step(u, u, A, Bt, Bt, state, slots=slots).any())
+    assert not bool(api.short_conv_step(u, ring, w, slots=slots).any())
+    assert torch.equal(state, s0) and torch.equal(ring, r0)
+
+
+def test_two_streams_and_two_graphs_side_by_side():
+    """Backward passes on two streams at once, and two captured ones replayed side by side, each with its own
+    workspace, give the bits of calls made one after the other."""
+    def case(seed):
+        c = scan_case(2, 48, 900, 16, 1, "bf16", seed, ("D", "bias", "gate"))
+        d = {k: c[k].cuda() for k in ("u", "delta", "A", "Bt", "Ct", "D", "dt_bias", "z", "dy")}
+
+        def run():
+            y, ck = api.selective_scan_fwd(d["u"], d["delta"], d["A"], d["Bt"], d["Ct"], d["D"], d["dt_bias"], d["z"],
+                                           return_ckpt=True)
+            g = api.selective_scan_bwd(d["dy"], d["u"], d["delta"], d["A"], d["Bt"], d["Ct"], ck, d["D"], d["dt_bias"],
+                                       d["z"])
+            return [y, *g]
+        return run
+    runs = [case(1), case(2)]
+    want = [[t.clone() for t in r()] for r in runs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [None, None]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                outs[i] = runs[i]()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert all(torch.equal(a, b) for a, b in zip(o, w))
+    graphs, res = [], []
+    for i, s in enumerate(streams):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            res.append(runs[i]())
+        graphs.append(g)
+    for _ in range(3):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(res, want):
+        assert all(torch.equal(a, b) for a, b in zip(o, w))
+
+
+def test_lengths_outside_the_row_count_as_its_ends():
+    c = scan_case(3, 6, 150, 4, 1, "f32", 31, ("D", "bias"))
+    a = [c[k].cuda() for k in ("u", "delta", "A", "Bt", "Ct", "D", "dt_bias")]
+    w = torch.randn(6, 4, generator=torch.Generator().manual_seed(2)).cuda()
+    n = torch.tensor([1000, -5, 40], dtype=torch.int32, device="cuda")
+    m = torch.tensor([150, 0, 40], dtype=torch.int32, device="cuda")
+    for f in (lambda k: api.selective_scan_fwd(*a, lengths=k, return_state=True),
+              lambda k: api.short_conv_fwd(a[0], w, lengths=k, return_state=True),
+              lambda k: api.short_conv_bwd(a[0], a[1], w, lengths=k)[:2]):
+        for x, y in zip(f(n), f(m)):
+            assert torch.equal(x, y)
