@@ -296,18 +296,29 @@ def _device(first: torch.Tensor, *others) -> torch.device:
     return dev
 
 
-class _Call:
-    """Makes `device` current for a call where it is not, and gives its current
-    stream's handle."""
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, device: torch.device):
-        self.index = device.index
-        self.guard = None if self.index == torch._C._cuda_getDevice() else torch.cuda.device(device)
+
+def _call(dev: torch.device, name: str, *args) -> None:
+    """Calls the library on the device's current stream, with the device current."""
+    if dev.index != _current_device():
+        with torch.cuda.device(dev):
+            return _call(dev, name, *args)
+    status = getattr(_lib.load(), name)(*args, _raw_stream(dev.index))
+    if status:
+        check(status, name)
+
+
+class _On:
+    """Makes a device current where it is not."""
+
+    def __init__(self, dev: torch.device):
+        self.guard = None if dev.index == _current_device() else torch.cuda.device(dev)
 
     def __enter__(self):
         if self.guard is not None:
             self.guard.__enter__()
-        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.guard is not None:
@@ -315,28 +326,27 @@ class _Call:
 
 
 def _check(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype) -> Optional[torch.Tensor]:
-    if t is not None:
+    if t is not None and not (t.dtype is dtype and t.shape == shape):
         if t.dtype is not dtype:
             raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t
 
 
 def _dense(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype):
     """A contiguous tensor of this shape and type, or None."""
-    if t is None:
-        return None
-    if _check(t, name, shape, dtype) is not None and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t
+    if t is None or (t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        return t
+    _check(t, name, shape, dtype)
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _seq(t: Optional[torch.Tensor], name: str, shape: tuple, dtype: torch.dtype):
     """A sequence of this shape and type with contiguous time, or None."""
-    if _check(t, name, shape, dtype) is not None and shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must be contiguous along its last axis")
-    return t
+    if t is None or (t.dtype is dtype and t.shape == shape and (t.stride(-1) == 1 or shape[-1] == 1)):
+        return t
+    _check(t, name, shape, dtype)
+    raise ValueError(f"{name} must be contiguous along its last axis")
 
 
 def _addr(t: Optional[torch.Tensor]):
@@ -393,10 +403,8 @@ def short_conv_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
     if out is None:
         out = torch.empty((B, H, L), dtype=x.dtype, device=dev)
     state = torch.empty((B, H, K - 1), dtype=x.dtype, device=dev) if return_state else None
-    with _Call(dev) as st:
-        check(_lib.load().short_conv_fwd(_addr(x), _addr(w), _addr(bias), _addr(out), B, H, L, K, bool(silu),
-                                         _addr(lengths), _strides(x.stride(0), x.stride(1)), _addr(state_in),
-                                         _addr(state), _DT[x.dtype], st), "short_conv_fwd")
+    _call(dev, "short_conv_fwd", _addr(x), _addr(w), _addr(bias), _addr(out), B, H, L, K, bool(silu), _addr(lengths),
+          _strides(x.stride(0), x.stride(1)), _addr(state_in), _addr(state), _DT[x.dtype])
     return (out, state) if return_state else out
 
 
@@ -429,12 +437,10 @@ def short_conv_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: Opt
     dw = torch.empty((H, K), dtype=torch.float32, device=dev)
     dbias = torch.empty((H,), dtype=torch.float32, device=dev) if bias is not None else None
     dstate = torch.empty((B, H, K - 1), dtype=io, device=dev) if need_dstate_in else None
-    with _Call(dev) as st:
-        check(lib.short_conv_bwd(_addr(dy), _addr(x), _addr(w), _addr(bias), _addr(out), _addr(dw), _addr(dbias), B, H,
-                                 L, K, bool(silu), _addr(lengths),
-                                 _strides(dy.stride(0), dy.stride(1), x.stride(0), x.stride(1)), _addr(state_in),
-                                 _addr(dstate_out), _addr(dstate), _addr(workspace),
-                                 workspace.numel() * workspace.element_size(), _DT[io], st), "short_conv_bwd")
+    _call(dev, "short_conv_bwd", _addr(dy), _addr(x), _addr(w), _addr(bias), _addr(out), _addr(dw), _addr(dbias), B, H,
+          L, K, bool(silu), _addr(lengths), _strides(dy.stride(0), dy.stride(1), x.stride(0), x.stride(1)),
+          _addr(state_in), _addr(dstate_out), _addr(dstate), _addr(workspace),
+          workspace.numel() * workspace.element_size(), _DT[io])
     return (out, dw, dbias, dstate) if need_dstate_in else (out, dw, dbias)
 
 
@@ -455,10 +461,8 @@ def short_conv_step(x: torch.Tensor, state: torch.Tensor, w: torch.Tensor, bias:
     dev = _device(x, w, bias, state, slots, out)
     if out is None:
         out = torch.empty((B, H), dtype=x.dtype, device=dev)
-    with _Call(dev) as st:
-        check(_lib.load().short_conv_step(_addr(x), _addr(state), _addr(w), _addr(bias), _addr(out), B, H, K,
-                                          bool(silu), _addr(slots), S, x.stride(0), _DT[x.dtype], st),
-              "short_conv_step")
+    _call(dev, "short_conv_step", _addr(x), _addr(state), _addr(w), _addr(bias), _addr(out), B, H, K, bool(silu),
+          _addr(slots), S, x.stride(0), _DT[x.dtype])
     return out
 
 
@@ -506,15 +510,14 @@ def selective_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bt
     ckpt = None
     if return_ckpt:
         ckpt = torch.empty(int(lib.selective_scan_ckpt_bytes(B, H, L, N)) // 4, dtype=torch.float32, device=dev)
-    with _Call(dev) as st:
+    with _On(dev):  # its size is that of the current device
         need = int(lib.selective_scan_workspace(B, H, L, N, G))
         if need or workspace is not None:
             workspace = _need(workspace, need, dev)
-        check(lib.selective_scan_fwd(_addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D), _addr(dt_bias),
-                                     _addr(z), _addr(out), B, H, L, N, G, bool(softplus), _addr(lengths),
-                                     _strides(*strides), _addr(state_in), _addr(state), _addr(ckpt), _addr(workspace),
-                                     0 if workspace is None else workspace.numel() * workspace.element_size(),
-                                     _DT[u.dtype], st), "selective_scan_fwd")
+    _call(dev, "selective_scan_fwd", _addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D), _addr(dt_bias),
+          _addr(z), _addr(out), B, H, L, N, G, bool(softplus), _addr(lengths), _strides(*strides), _addr(state_in),
+          _addr(state), _addr(ckpt), _addr(workspace),
+          0 if workspace is None else workspace.numel() * workspace.element_size(), _DT[u.dtype])
     more = ((state,) if return_state else ()) + ((ckpt,) if return_ckpt else ())
     return (out, *more) if more else out
 
@@ -553,15 +556,13 @@ def selective_scan_bwd(dy: torch.Tensor, u: torch.Tensor, delta: torch.Tensor, A
     dB, dC, dA = new(B, G, N, L, dtype=io), new(B, G, N, L, dtype=io), new(H, N)
     dD, dbias = new(H, when=D is not None), new(H, when=dt_bias is not None)
     dstate = new(B, H, N, when=need_dstate_in)
-    with _Call(dev) as st:
+    with _On(dev):  # its size is that of the current device
         workspace = _need(workspace, int(lib.selective_scan_bwd_workspace(B, H, L, N, G)), dev)
-        check(lib.selective_scan_bwd(_addr(dy), _addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D),
-                                     _addr(dt_bias), _addr(z), _addr(ckpt), _addr(du), _addr(ddelta), _addr(dA),
-                                     _addr(dB), _addr(dC), _addr(dD), _addr(dbias), _addr(dz), B, H, L, N, G,
-                                     bool(softplus), _addr(lengths), _strides(dy.stride(0), dy.stride(1), *strides),
-                                     _addr(dstate_out), _addr(dstate), _addr(workspace),
-                                     workspace.numel() * workspace.element_size(), _DT[io], st),
-              "selective_scan_bwd")
+    _call(dev, "selective_scan_bwd", _addr(dy), _addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D),
+          _addr(dt_bias), _addr(z), _addr(ckpt), _addr(du), _addr(ddelta), _addr(dA), _addr(dB), _addr(dC), _addr(dD),
+          _addr(dbias), _addr(dz), B, H, L, N, G, bool(softplus), _addr(lengths),
+          _strides(dy.stride(0), dy.stride(1), *strides), _addr(dstate_out), _addr(dstate), _addr(workspace),
+          workspace.numel() * workspace.element_size(), _DT[io])
     grads = (du, ddelta, dA, dB, dC, dD, dbias, dz)
     return (*grads, dstate) if need_dstate_in else grads
 
@@ -582,11 +583,9 @@ def selective_scan_step(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B
     dev = _device(u, delta, A, Bt, Ct, D, dt_bias, z, state, slots, out)
     if out is None:
         out = torch.empty((B, H), dtype=u.dtype, device=dev)
-    with _Call(dev) as st:
-        check(_lib.load().selective_scan_step(_addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D),
-                                              _addr(dt_bias), _addr(z), _addr(state), _addr(out), B, H, N, G,
-                                              bool(softplus), _addr(slots), S, _strides(*strides), _DT[u.dtype], st),
-              "selective_scan_step")
+    _call(dev, "selective_scan_step", _addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D), _addr(dt_bias),
+          _addr(z), _addr(state), _addr(out), B, H, N, G, bool(softplus), _addr(slots), S, _strides(*strides),
+          _DT[u.dtype])
     return out
 
 
@@ -613,10 +612,8 @@ def group_norm_act_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tens
     dev = _device(x, weight, bias, gate, out)
     if out is None:
         out = torch.empty((B, L, C), dtype=x.dtype, device=dev)
-    with _Call(dev) as st:
-        check(_lib.load().group_norm_act_fwd(_addr(x), _addr(weight), _addr(bias), _addr(gate), _addr(out), B, L, C,
-                                             groups, eps, bool(channel_major), _DT[x.dtype], st),
-              "group_norm_act_fwd")
+    _call(dev, "group_norm_act_fwd", _addr(x), _addr(weight), _addr(bias), _addr(gate), _addr(out), B, L, C, groups,
+          eps, bool(channel_major), _DT[x.dtype])
     return out
 
 
@@ -637,10 +634,9 @@ def group_norm_act_bwd(dy: torch.Tensor, x: torch.Tensor, groups: int, weight: O
     dgate = torch.empty_like(gate) if gate is not None else None
     dw = torch.empty((C,), dtype=torch.float32, device=dev) if weight is not None else None
     db = torch.empty((C,), dtype=torch.float32, device=dev) if bias is not None else None
-    with _Call(dev) as st:
+    with _On(dev):  # its size is that of the current device
         workspace = _need(workspace, int(lib.group_norm_act_bwd_workspace(B, L, C, groups, bool(channel_major))), dev)
-        check(lib.group_norm_act_bwd(_addr(dy), _addr(x), _addr(weight), _addr(bias), _addr(gate), _addr(dx), _addr(dw),
-                                     _addr(db), _addr(dgate), B, L, C, groups, eps, bool(channel_major),
-                                     _addr(workspace), workspace.numel() * workspace.element_size(), _DT[x.dtype], st),
-              "group_norm_act_bwd")
+    _call(dev, "group_norm_act_bwd", _addr(dy), _addr(x), _addr(weight), _addr(bias), _addr(gate), _addr(dx),
+          _addr(dw), _addr(db), _addr(dgate), B, L, C, groups, eps, bool(channel_major), _addr(workspace),
+          workspace.numel() * workspace.element_size(), _DT[x.dtype])
     return dx, dw, db, dgate
