@@ -484,7 +484,8 @@ bool rows_of(fc::Rows* r, const void* p, const long long* st, bool grouped, int 
   }
   if (r->bs < 0 || r->rs < 0 || r->gs < 0) return false;
   if (r->bs > lim / B || r->gs > lim / G || r->rs > lim / R) return false;
-  r->vec = aligned(p, 16) && r->bs % per16 == 0 && r->rs % per16 == 0 && r->gs % per16 == 0;
+  r->vec = aligned(p, 16) && (B == 1 || r->bs % per16 == 0) && (R == 1 || r->rs % per16 == 0) &&
+           (G == 1 || r->gs % per16 == 0);
   return true;
 }
 
@@ -764,8 +765,9 @@ FC_API fc_status selective_scan_step(const void* u, const void* delta, const flo
 // ------------------------------------------------------------------ group norm with SiLU
 static fc_status check_norm(const void* x, const float* w, const float* bias, const void* gate, int B, int L, int C,
                             int G, float eps, int dtype) {
-  fc_status s = check_sizes(B, C, L, dtype);
-  if (s != FC_OK) return s;
+  FC_REQUIRE(dtype_ok(dtype), FC_EINVAL, "unknown dtype %d", dtype);
+  FC_REQUIRE(B >= 1 && L >= 1 && C >= 1, FC_EINVAL, "B, L, C must be >= 1 (got %d, %d, %d)", B, L, C);
+  FC_REQUIRE(L <= kMaxSteps, FC_EUNSUPPORTED, "L = %d > 2^30", L);
   FC_REQUIRE(G >= 1 && C % G == 0, FC_EINVAL, "C = %d is not a multiple of G = %d", C, G);
   FC_REQUIRE(C / G <= 8192, FC_EUNSUPPORTED, "C / G = %d > 8192", C / G);
   FC_REQUIRE(G <= 65535 && C <= (1 << 28), FC_EUNSUPPORTED, "G = %d > 65535 or C = %d > 2^28", G, C);

@@ -110,8 +110,10 @@ struct Group {
     const T* q = (const T*)base + off;
     if (FULL && vec) {
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        r[v] = Raw8<T>{};
         if (on) ldraw8(q + (v * P + lane) * 8, r[v]);
+      }
       return;
     }
 #pragma unroll
@@ -226,12 +228,6 @@ __global__ __launch_bounds__(kThreads, V == 1 ? kBwdBlocks : 1) void norm_bwd_ke
       xn.get(v, x[v]);
       yn.get(v, dn[v]);
       if (GATE) zn.get(v, z[v]);
-    }
-    if (FULL && !live) {  // what the last load left
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dn[v][i] = make_float2(0.f, 0.f);
     }
     load(off + step, unit + stride < units);
     stats<BLOCK, FULL, V>(x, lane, P, p, red, mean, rstd);

@@ -52,14 +52,16 @@ __device__ __forceinline__ void fetch8(T* slot, const T* row, long long t0, int 
 #pragma unroll
     for (int i = 0; i < (int)sizeof(T) / 2; ++i)
       asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(shared_addr(slot) + 16 * i),
-                   "l"((const char*)(row + t0) + 16 * i));
+                   "l"((const char*)(row + t0) + 16 * i)
+                   : "memory");
     return;
   }
   if constexpr (sizeof(T) == 4) {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       if (t0 + i < n)
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_addr(slot + i)), "l"(row + t0 + i));
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_addr(slot + i)), "l"(row + t0 + i)
+                   : "memory");
       else
         slot[i] = T(0.f);
   } else if (inner8(t0, L)) {

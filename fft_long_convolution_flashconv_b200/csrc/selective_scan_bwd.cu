@@ -201,7 +201,8 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_bwd_kernel(ScanArgs
     float* d = &sm.ck[it & 1][tid % kStates][cc];
     if (s < N && tile * CH + cc < E)
       asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(shared_addr(d)),
-                   "l"(q.ckpt + (((long long)b * p.H + g * E + tile * CH + cc) * nck + k) * N + s));
+                   "l"(q.ckpt + (((long long)b * p.H + g * E + tile * CH + cc) * nck + k) * N + s)
+                   : "memory");
     else
       *d = 0.f;
   };

@@ -416,8 +416,8 @@ FC_API fc_status selective_scan_step(const void* u, const void* delta, const flo
  *   group of one token;  y = silu(n), or n silu(gate) with a gate
  * x, gate: B x L x C (h3_mixer_fwd's output), or with channel_major B x C x L
  * (selective_scan_fwd's output); y: B x L x C; weight, bias: C floats or NULL
- * (1, 0).  All contiguous and 16-byte aligned.  Limits: C / G <= 8192, G <=
- * 65535, B * L * G < 2^31, eps > 0.  Precision: float32 (mean first, then the
+ * (1, 0).  All contiguous and 16-byte aligned.  Limits: L <= 2^30, C <= 2^28,
+ * C / G <= 8192, G <= 65535, B * L * G < 2^31, eps > 0.  Precision: float32 (mean first, then the
  * squares around it), y rounded once. */
 FC_API fc_status group_norm_act_fwd(const void* x, const float* weight, const float* bias, const void* gate, void* y,
                                     int B, int L, int C, int G, float eps, int channel_major, fc_dtype dtype,

@@ -474,6 +474,8 @@ def norm_ref(x, G, w, bias, gate, eps):
     (1, 3, 8192, 1, "f32", ("w", "b", "gate")),
     (4, 300, 64, 1, "f16", ("w", "b", "gate")),
     (1, 33, 36, 3, "f32", ("w", "b")),             # groups of 12
+    (1, 1, 64, 1, "f16", ("w", "b", "gate")),      # one group: most of its block has nothing to do
+    (1, 3, 32, 2, "f32", ("w", "b")),
     (2, 128, 32, 1, "bf16", ("w", "b", "gate")),   # whole tiles of tokens and channels
     (1, 192, 256, 2, "f16", ("w", "b")),
     (1, 64, 512, 2, "f32", ("w", "gate")),
