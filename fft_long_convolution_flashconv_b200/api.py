@@ -401,8 +401,8 @@ def short_conv_fwd(x: torch.Tensor, w: torch.Tensor, bias: Optional[torch.Tensor
     _dense(out, "out", (B, H, L), x.dtype)
     dev = _device(x, w, bias, state_in, lengths, out)
     if out is None:
-        out = torch.empty((B, H, L), dtype=x.dtype, device=dev)
-    state = torch.empty((B, H, K - 1), dtype=x.dtype, device=dev) if return_state else None
+        out = x.new_empty((B, H, L))
+    state = x.new_empty((B, H, K - 1)) if return_state else None
     _call(dev, "short_conv_fwd", _addr(x), _addr(w), _addr(bias), _addr(out), B, H, L, K, bool(silu), _addr(lengths),
           _strides(x.stride(0), x.stride(1)), _addr(state_in), _addr(state), _DT[x.dtype])
     return (out, state) if return_state else out
@@ -433,10 +433,10 @@ def short_conv_bwd(dy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, bias: Opt
     lib = _lib.load()
     workspace = _need(workspace, int(lib.short_conv_bwd_workspace(B, H, L, K)), dev)
     if out is None:
-        out = torch.empty((B, H, L), dtype=io, device=dev)
+        out = x.new_empty((B, H, L))
     dw = torch.empty((H, K), dtype=torch.float32, device=dev)
     dbias = torch.empty((H,), dtype=torch.float32, device=dev) if bias is not None else None
-    dstate = torch.empty((B, H, K - 1), dtype=io, device=dev) if need_dstate_in else None
+    dstate = x.new_empty((B, H, K - 1)) if need_dstate_in else None
     _call(dev, "short_conv_bwd", _addr(dy), _addr(x), _addr(w), _addr(bias), _addr(out), _addr(dw), _addr(dbias), B, H,
           L, K, bool(silu), _addr(lengths), _strides(dy.stride(0), dy.stride(1), x.stride(0), x.stride(1)),
           _addr(state_in), _addr(dstate_out), _addr(dstate), _addr(workspace),
@@ -460,7 +460,7 @@ def short_conv_step(x: torch.Tensor, state: torch.Tensor, w: torch.Tensor, bias:
     _dense(out, "out", (B, H), x.dtype)
     dev = _device(x, w, bias, state, slots, out)
     if out is None:
-        out = torch.empty((B, H), dtype=x.dtype, device=dev)
+        out = x.new_empty((B, H))
     _call(dev, "short_conv_step", _addr(x), _addr(state), _addr(w), _addr(bias), _addr(out), B, H, K, bool(silu),
           _addr(slots), S, x.stride(0), _DT[x.dtype])
     return out
@@ -505,7 +505,7 @@ def selective_scan_fwd(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, Bt
     dev = _device(u, delta, A, Bt, Ct, D, dt_bias, z, state_in, lengths, out)
     lib = _lib.load()
     if out is None:
-        out = torch.empty((B, H, L), dtype=u.dtype, device=dev)
+        out = u.new_empty((B, H, L))
     state = torch.empty((B, H, N), dtype=torch.float32, device=dev) if return_state else None
     ckpt = None
     if return_ckpt:
@@ -582,7 +582,7 @@ def selective_scan_step(u: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B
     _dense(out, "out", (B, H), u.dtype)
     dev = _device(u, delta, A, Bt, Ct, D, dt_bias, z, state, slots, out)
     if out is None:
-        out = torch.empty((B, H), dtype=u.dtype, device=dev)
+        out = u.new_empty((B, H))
     _call(dev, "selective_scan_step", _addr(u), _addr(delta), _addr(A), _addr(Bt), _addr(Ct), _addr(D), _addr(dt_bias),
           _addr(z), _addr(state), _addr(out), B, H, N, G, bool(softplus), _addr(slots), S, _strides(*strides),
           _DT[u.dtype])
@@ -611,7 +611,7 @@ def group_norm_act_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tens
     _dense(out, "out", (B, L, C), x.dtype)
     dev = _device(x, weight, bias, gate, out)
     if out is None:
-        out = torch.empty((B, L, C), dtype=x.dtype, device=dev)
+        out = x.new_empty((B, L, C))
     _call(dev, "group_norm_act_fwd", _addr(x), _addr(weight), _addr(bias), _addr(gate), _addr(out), B, L, C, groups,
           eps, bool(channel_major), _DT[x.dtype])
     return out

@@ -58,23 +58,37 @@ __device__ __forceinline__ void ldraw8(const T* p, Raw8<T>& r) {
   r.a = __ldg(reinterpret_cast<const uint4*>(p));
 }
 
-// The eight elements from p on, p not on a 16-byte boundary: the two aligned
-// vectors around them, moved down by p's offset in the first.  Both vectors have
-// to lie in the row (see inner8).
+// Eight 16-bit elements from an address on a two-byte boundary: the two aligned
+// vectors around them, moved down by the address's offset in the first.  Both have
+// to lie in the row (see inner8).  In two halves, so that several rows' loads can be
+// on their way together.
+template <typename T>
+struct Wide {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const T* p) {
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) & ~(uintptr_t)15);
+    a = __ldg(q);
+    b = __ldg(q + 1);
+  }
+  __device__ __forceinline__ void put(T* slot, const T* p) const {  // eight elements at a 16-byte boundary
+    const uint32_t m = (uint32_t)(reinterpret_cast<uintptr_t>(p) & 15);
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
+    const uint32_t sh = (m & 2) * 8;
+    *reinterpret_cast<uint4*>(slot) =
+        make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh), __funnelshift_r(w[2], w[3], sh),
+                   __funnelshift_r(w[3], w[4], sh));
+  }
+};
 template <typename T>
 __device__ __forceinline__ void ldraw8_any(const T* p, Raw8<T>& r) {
   static_assert(sizeof(T) == 2, "two 16-byte vectors hold eight 16-bit elements at any offset");
-  const uintptr_t m = reinterpret_cast<uintptr_t>(p) & 15;
-  const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<uintptr_t>(p) - m);
-  const uint4 a = __ldg(q), b = __ldg(q + 1);
-  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 6; ++i) w[i] = m & 8 ? w[i + 2] : w[i];
-#pragma unroll
-  for (int i = 0; i < 5; ++i) w[i] = m & 4 ? w[i + 1] : w[i];
-  const uint32_t sh = (uint32_t)(m & 2) * 8;
-  r.a = make_uint4(__funnelshift_r(w[0], w[1], sh), __funnelshift_r(w[1], w[2], sh), __funnelshift_r(w[2], w[3], sh),
-                   __funnelshift_r(w[3], w[4], sh));
+  Wide<T> w;
+  w.load(p);
+  w.put(reinterpret_cast<T*>(&r), p);
 }
 __device__ __forceinline__ bool inner8(long long t0, int L) { return t0 >= 8 && t0 + 16 <= L; }
 

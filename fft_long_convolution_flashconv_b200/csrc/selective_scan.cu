@@ -63,6 +63,25 @@ struct Tiles {
       }
     }
   }
+  // The same of rows on two-byte boundaries, where the block lies inside the sequence: all loads before the first
+  // is used (threads without a row of their own repeat the last).
+  __device__ __forceinline__ void fetch_odd(const ScanArgs& p, int s0, int ns, int tb) const {
+    Wide<T> b[kPer], c[kPer];
+    long long at[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = threadIdx.x + j * kThreads;
+      at[j] = s0 + min(i / kRow, ns - 1);
+      b[j].load(Bt + at[j] * p.Bt.rs + tb + i % kRow * 8);
+      c[j].load(Ct + at[j] * p.Ct.rs + tb + i % kRow * 8);
+    }
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int i = threadIdx.x + j * kThreads;
+      b[j].put(slot + j * 8, Bt + at[j] * p.Bt.rs + tb + i % kRow * 8);
+      c[j].put(slot + (kPer + j) * 8, Ct + at[j] * p.Ct.rs + tb + i % kRow * 8);
+    }
+  }
   // Rows from ns on, which fill up a group of states, are zeros.
   __device__ __forceinline__ void store(float* buf, int ns, int tb, int n) const {
 #pragma unroll
@@ -192,7 +211,8 @@ struct Layout {
 };
 
 // A block of four warps takes CH channels of a group.
-template <typename T, int TPL, bool CKPT>
+// ODD: 16-bit rows, none of them on 16-byte boundaries (an odd L, mostly).
+template <typename T, int TPL, bool CKPT, bool ODD>
 __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, Segments sg, T* y,
                                                                                 float* state_out, float* ckpt,
                                                                                 int tiles) {
@@ -291,17 +311,49 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_kernel(ScanArgs p, 
   int it = 0;
   for (int k = first; k < end; ++k) {
     steps(k);
-    if (z) {
+    // Rows on two-byte boundaries inside the sequence: this block's gate, the next one's u and delta and the next B
+    // and C tile, loaded together.
+    const bool together = ODD && k > 0 && k + 1 < end && (k + 2) * TB + 8 <= p.L;
+    if (together) {
+      if constexpr (ODD) {
+        const T* zz = z ? z : u;
+        Wide<T> q[3][VPL];
 #pragma unroll
-      for (int j = 0; j < VPL; ++j) fetch8(slot(4, j), z, k * TB + tl * TPL + j * 8, p.L, n, p.z.vec);
+        for (int j = 0; j < VPL; ++j) {
+          const int t0 = k * TB + tl * TPL + j * 8;
+          q[0][j].load(u + t0 + TB);
+          q[1][j].load(delta + t0 + TB);
+          q[2][j].load(zz + t0);
+        }
+        next.fetch_odd(p, chunks > 1 ? kStates : 0, min(N - (chunks > 1 ? kStates : 0), kStates),
+                       (chunks > 1 ? k : k + 1) * TB);
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) {
+          const int t0 = k * TB + tl * TPL + j * 8;
+          q[0][j].put(slot(((k + 1) & 1) * 2, j), u + t0 + TB);
+          q[1][j].put(slot(((k + 1) & 1) * 2 + 1, j), delta + t0 + TB);
+          q[2][j].put(slot(4, j), zz + t0);
+        }
+      }
+    } else {
+      if (z) {
+#pragma unroll
+        for (int j = 0; j < VPL; ++j) fetch8(slot(4, j), z, k * TB + tl * TPL + j * 8, p.L, n, p.z.vec);
+      }
+      if (k + 1 < end) fetch(k + 1);
     }
-    if (k + 1 < end) fetch(k + 1);
     float* ck = CKPT ? ckpt + (((long long)b * p.H + h) * nck + k) * N : nullptr;
     for (int ch = 0; ch < chunks; ++ch, ++it) {
       const int s0 = ch * kStates, ns = min(N - s0, kStates);
       const bool more = ch + 1 < chunks || k + 1 < end;
       const int sn = ch + 1 < chunks ? s0 + kStates : 0, tbn = (ch + 1 < chunks ? k : k + 1) * TB;
-      if (more) next.fetch(p, sn, min(N - sn, kStates), tbn, n);
+      if (more && !(together && ch == 0)) {
+        if (ODD && k > 0 && (k + 2) * TB + 8 <= p.L) {
+          if constexpr (ODD) next.fetch_odd(p, sn, min(N - sn, kStates), tbn);
+        } else {
+          next.fetch(p, sn, min(N - sn, kStates), tbn, n);
+        }
+      }
       const float* Bs = bc + (it & 1) * 2 * kStates * TB;
 #pragma unroll S::kUnroll
       for (int e = 0; e < ns; e += SG)
@@ -443,24 +495,33 @@ __global__ __launch_bounds__(kThreads) void scan_step_kernel(ScanArgs p, float* 
   }
 }
 
-template <typename T, int TPL, bool CKPT>
+template <typename T, int TPL, bool CKPT, bool ODD>
 cudaError_t run(const ScanArgs& p, const Segments& sg, void* y, float* state_out, float* ckpt, cudaStream_t st) {
   constexpr int CH = Shape<TPL>::CH;
   const int tiles = (p.H / p.G + CH - 1) / CH;
   const size_t smem = Layout<T, TPL>::bytes((p.N + kStates - 1) / kStates * kStates);
-  const cudaError_t e = smem_optin<scan_kernel<T, TPL, CKPT>>(smem);
+  const cudaError_t e = smem_optin<scan_kernel<T, TPL, CKPT, ODD>>(smem);
   if (e != cudaSuccess) return e;
-  scan_kernel<T, TPL, CKPT><<<(unsigned)((long long)tiles * p.B * p.G * sg.count), kThreads, smem, st>>>(
+  scan_kernel<T, TPL, CKPT, ODD><<<(unsigned)((long long)tiles * p.B * p.G * sg.count), kThreads, smem, st>>>(
       p, sg, (T*)y, state_out, ckpt, tiles);
   return cudaGetLastError();
+}
+template <typename T, int TPL>
+cudaError_t run(const ScanArgs& p, const Segments& sg, void* y, float* state_out, float* ckpt, cudaStream_t st) {
+  if constexpr (sizeof(T) == 2) {
+    // a kernel of its own (8 x 768 x 2047, fp16: 200 -> 171 us; the branch in the other one cost 3 to 4%)
+    if (!p.u.vec && !p.delta.vec && !(p.z.p && p.z.vec) && !p.Bt.vec && !p.Ct.vec)
+      return ckpt ? run<T, TPL, true, true>(p, sg, y, state_out, ckpt, st)
+                  : run<T, TPL, false, true>(p, sg, y, state_out, nullptr, st);
+  }
+  return ckpt ? run<T, TPL, true, false>(p, sg, y, state_out, ckpt, st)
+              : run<T, TPL, false, false>(p, sg, y, state_out, nullptr, st);
 }
 
 template <typename T>
 cudaError_t fwd(const ScanArgs& p, int tpl, const Segments& sg, void* y, float* state_out, float* ckpt,
                 cudaStream_t st) {
-  if (tpl == 8)
-    return ckpt ? run<T, 8, true>(p, sg, y, state_out, ckpt, st) : run<T, 8, false>(p, sg, y, state_out, nullptr, st);
-  return ckpt ? run<T, 16, true>(p, sg, y, state_out, ckpt, st) : run<T, 16, false>(p, sg, y, state_out, nullptr, st);
+  return tpl == 8 ? run<T, 8>(p, sg, y, state_out, ckpt, st) : run<T, 16>(p, sg, y, state_out, ckpt, st);
 }
 
 struct Plan {
