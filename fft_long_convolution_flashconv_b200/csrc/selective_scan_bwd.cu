@@ -34,6 +34,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kStates = 8;  // states whose tiles are in shared memory at a time
+constexpr int kLaneStates = 16;  // up to so many states a lane keeps its own dA (8 KB: four blocks an SM still fit)
 constexpr int kMinBlocks = 4;  // resident on an SM: 128 registers a thread
 constexpr int TPL = 8, TL = 8, CL = 4, TB = kCkptSteps, CH = kWarps * CL, PAIRS = TPL / 2;
 static_assert(TB == TL * TPL, "a block of steps is what a channel's lanes hold");
@@ -115,7 +116,8 @@ struct Sm {
   float sums[kWarps][kStates][2][TB];               // dB, dC of a warp's channels
   float ck[2][kStates][CH];                         // states entering the block
   float zero[kStates][CH];                          // for the lanes that none enters
-  // [Np][CH] each: A, dA, what nothing reads, entering adjoint, what nothing reads
+  // [Np][CH] each: A, entering adjoint, what nothing reads; then dA, of every lane ([Np][kThreads], up to kLaneStates
+  // states) or of the channels (twice [Np][CH], the second never read)
 };
 
 template <typename T>
@@ -124,8 +126,9 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_bwd_kernel(ScanArgs
   Sm<T>& sm = *reinterpret_cast<Sm<T>*>(smem4);
   const int N = p.N, chunks = (N + kStates - 1) / kStates, Np = chunks * kStates;
   float* const As = reinterpret_cast<float*>(&sm + 1);  // [Np][CH]
-  float* const das = As + Np * CH;                      // as large each, and as much behind them that nothing reads
-  float* const gs = das + 2 * Np * CH;
+  float* const gs = As + Np * CH;  // as large, and as much behind it that nothing reads
+  float* const das = gs + 2 * Np * CH;
+  const bool lanes = Np <= kLaneStates;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, tl = lane / CL, cl = lane % CL, c = warp * CL + cl;
   const int E = p.H / p.G;
   const int seg = blockIdx.x % sg.count, tile = blockIdx.x / sg.count % tiles, bg = blockIdx.x / sg.count / tiles;
@@ -143,10 +146,11 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_bwd_kernel(ScanArgs
             : sg.state     ? __ldg(sg.state + (r * sg.count + seg) * N + s)
             : q.dstate_out ? __ldg(q.dstate_out + r * N + s)
                            : 0.f;
-    das[i] = das[Np * CH + i] = 0.f;
     if (i < kStates * CH) sm.zero[0][i] = 0.f;
   }
-  float* const da_at = das + (tl == 0 ? 0 : Np * CH) + c;
+  for (int i = tid; i < Np * (lanes ? kThreads : 2 * CH); i += kThreads) das[i] = 0.f;
+  float* const da_at = das + (lanes ? tid : (tl == 0 ? 0 : Np * CH) + c);
+  const int da_step = lanes ? kThreads : CH;
   const uint32_t r1s = shared_addr(tl == 0 ? gs + c : gs + Np * CH + c);
   const T* u = (const T*)p.u.p + b * p.u.bs + h * p.u.rs;
   const T* delta = (const T*)p.delta.p + b * p.delta.bs + h * p.delta.rs;
@@ -253,7 +257,11 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_bwd_kernel(ScanArgs
       if (z) {
         take8(sm.in[k & 1][3][tid], t0, m, d);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] *= silu(d[i]);
+        for (int i = 0; i < PAIRS; ++i) {
+          const float2 g2 = mul2(pair(e, i), silu2(pair(d, i)));
+          e[2 * i] = g2.x;
+          e[2 * i + 1] = g2.y;
+        }
       }
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i) {
@@ -343,53 +351,70 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_bwd_kernel(ScanArgs
         }
         *reinterpret_cast<float2*>(out) = sum_channels(v, cl);
         float d = da.x + da.y;
+        if (!lanes) {
 #pragma unroll
-        for (int e = CL; e < 32; e *= 2) d += __shfl_xor_sync(~0u, d, e);
-        da_at[(s0 + s) * CH] += d;
+          for (int e = CL; e < 32; e *= 2) d += __shfl_xor_sync(~0u, d, e);
+        }
+        da_at[(s0 + s) * da_step] += d;
       }
       if (more) commit_tile(kn, cn, it + 1);
       __syncthreads();
-      for (int i = tid; i < ns * 2 * TB; i += kThreads) {
-        const int t = k * TB + i % TB;
-        float v = 0.f;
+      for (int i = tid; i < ns * 2 * (TB / 4); i += kThreads) {  // four steps of dB or dC of a state
+        const float4* q = reinterpret_cast<const float4*>(&sm.sums[0][0][0][0]) + i;
+        constexpr int kWarp4 = kStates * 2 * TB / 4;
+        float4 v = q[0];
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v += (&sm.sums[w][0][0][0])[i];
-        if (t < p.L) pbc[(i / TB & 1) * pstep + (long long)(s0 + i / (2 * TB)) * p.L + t] = v;
+        for (int w = 1; w < kWarps; ++w) {
+          const float4 o = q[w * kWarp4];
+          v = make_float4(v.x + o.x, v.y + o.y, v.z + o.z, v.w + o.w);
+        }
+        const int t = k * TB + i % (TB / 4) * 4, row = i / (TB / 4);
+        float* o = pbc + (row & 1) * pstep + (long long)(s0 + row / 2) * p.L + t;
+        if (p.L % 4 == 0) {
+          if (t < p.L) *reinterpret_cast<float4*>(o) = v;
+        } else {
+          if (t < p.L) o[0] = v.x;
+          if (t + 1 < p.L) o[1] = v.y;
+          if (t + 2 < p.L) o[2] = v.z;
+          if (t + 3 < p.L) o[3] = v.w;
+        }
       }
       __syncthreads();
     }
     if (live && t0 < p.L) {
       float v[8], o[8], w[8];
       take8(sm.in[k & 1][0][tid], t0, n, v);
-      float sd = 0.f, sb = 0.f;
+      float2 sd = make_float2(0.f, 0.f), sb = sd;
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i) {
-        o[2 * i] = fmaf(dt[i].x, gB[i].x, Dh * dyp[i].x);
-        o[2 * i + 1] = fmaf(dt[i].y, gB[i].y, Dh * dyp[i].y);
-        sd = fmaf(dyp[i].x, v[2 * i], fmaf(dyp[i].y, v[2 * i + 1], sd));
+        const float2 g2 = fma2(dt[i], gB[i], mul2(both(Dh), dyp[i]));
+        o[2 * i] = g2.x;
+        o[2 * i + 1] = g2.y;
+        sd = fma2(dyp[i], pair(v, i), sd);
       }
-      sum_d += sd;
+      sum_d += sd.x + sd.y;
       store8((T*)q.du + row * p.L, t0, p.L, n, p.out_vec, o);
       take8(sm.in[k & 1][1][tid], t0, n, w);
 #pragma unroll
       for (int i = 0; i < PAIRS; ++i) {
-        o[2 * i] = fmaf(v[2 * i], gB[i].x, gA[i].x);
-        o[2 * i + 1] = fmaf(v[2 * i + 1], gB[i].y, gA[i].y);
+        float2 g2 = fma2(pair(v, i), gB[i], gA[i]);
+        if (p.softplus) g2 = mul2(g2, sigmoid2(add2(pair(w, i), both(bias))));
+        if (t0 + 2 * i >= n) g2.x = 0.f;
+        if (t0 + 2 * i + 1 >= n) g2.y = 0.f;
+        sb = add2(sb, g2);
+        o[2 * i] = g2.x;
+        o[2 * i + 1] = g2.y;
       }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (p.softplus) o[i] *= sigmoid(w[i] + bias);
-        if (t0 + i < n) sb += o[i];
-      }
-      sum_bias += sb;
+      sum_bias += sb.x + sb.y;
       store8((T*)q.ddelta + row * p.L, t0, p.L, n, p.out_vec, o);
       if (z) {
         take8(sm.in[k & 1][2][tid], t0, n, v);
         take8(sm.in[k & 1][3][tid], t0, n, w);
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
-          o[2 * i] = v[2 * i] * y0[i].x * dsilu(w[2 * i]);
-          o[2 * i + 1] = v[2 * i + 1] * y0[i].y * dsilu(w[2 * i + 1]);
+          const float2 g2 = mul2(mul2(pair(v, i), y0[i]), dsilu2(pair(w, i)));
+          o[2 * i] = g2.x;
+          o[2 * i + 1] = g2.y;
         }
         store8((T*)q.dz + row * p.L, t0, p.L, n, p.out_vec, o);
       }
@@ -409,7 +434,14 @@ __global__ __launch_bounds__(kThreads, kMinBlocks) void scan_bwd_kernel(ScanArgs
   for (int i = tid; i < N * CH; i += kThreads) {
     const int cc = i / N, s = i % N, hh = g * E + tile * CH + cc;
     if (tile * CH + cc >= E) continue;
-    q.part_a[(part * p.H + hh) * N + s] = das[s * CH + cc];
+    float v = 0.f;
+    if (lanes) {
+#pragma unroll
+      for (int j = 0; j < TL; ++j) v += das[s * kThreads + cc / CL * 32 + j * CL + cc % CL];
+    } else {
+      v = das[s * CH + cc];
+    }
+    q.part_a[(part * p.H + hh) * N + s] = v;
     if (q.dstate_in && seg == 0) q.dstate_in[((long long)b * p.H + hh) * N + s] = gs[s * CH + cc];
   }
 }
@@ -484,7 +516,7 @@ cudaError_t bwd(const ScanArgs& p, BwdOut q, void* dB, void* dC, float* dA, floa
   cudaError_t e;
   if (pl.sg.count > 1 && (e = launch_segment_states(p, pl.sg, q.dstate_out, true, dtype, st)) != cudaSuccess) return e;
   const int Np = (p.N + kStates - 1) / kStates * kStates;
-  const size_t smem = sizeof(Sm<T>) + (size_t)5 * Np * CH * 4;
+  const size_t smem = sizeof(Sm<T>) + (size_t)Np * (3 * CH + (Np <= kLaneStates ? kThreads : 2 * CH)) * 4;
   e = smem_optin<scan_bwd_kernel<T>>(smem);
   if (e != cudaSuccess) return e;
   scan_bwd_kernel<T><<<(unsigned)((long long)pl.tiles * p.B * p.G * pl.sg.count), kThreads, smem, st>>>(p, q, pl.sg,
