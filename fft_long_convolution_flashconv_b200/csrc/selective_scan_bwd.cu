@@ -491,8 +491,8 @@ Plan plan(int B, int H, int L, int N, int G) {
   for (int want = 1; want <= 64 && (want == 1 || ctas * (want - 1) < 16 * sms); ++want) {
     const int blocks = (all + want - 1) / want, count = (all + blocks - 1) / blocks;
     if (count != want || (count > 1 && blocks < 4)) continue;
-    // measured: 144 us and 89 us for each thread block on an SM, 2048 steps of 16 states in bf16
-    const float t = scan_cost(ctas * count, blocks, kMinBlocks, 144.f, 89.f, sms) +
+    // measured: 130 us and 80 us for each thread block on an SM, 2048 steps of 16 states in bf16
+    const float t = scan_cost(ctas * count, blocks, kMinBlocks, 130.f, 80.f, sms) +
                     (count > 1 ? ends_cost(B, H, G, N, count, blocks, sms) : 0.f);
     if (least < 0.f || t < least) {
       least = t;
