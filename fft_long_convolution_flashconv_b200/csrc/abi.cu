@@ -466,6 +466,7 @@ FC_TEST_API unsigned int fc_debug_tc_timeouts(void) { return fc_tc_timeouts(); }
 namespace {
 
 constexpr int kMaxSteps = 1 << 30;  // sequence length: vector offsets stay in an int
+constexpr int kMaxChannels = 1 << 30;  // so that a block's last channel, past H, stays in an int
 
 // A strided input of B x R rows of `len` contiguous elements, in G groups (group stride st[1], row stride st[2]; G == 1
 // without groups: st = batch, row).  False for a negative stride or an extent past 2^60 elements.
@@ -504,6 +505,7 @@ fc_status check_sizes(int B, int H, int L, int dtype) {
   FC_REQUIRE(dtype_ok(dtype), FC_EINVAL, "unknown dtype %d", dtype);
   FC_REQUIRE(B >= 1 && H >= 1 && L >= 1, FC_EINVAL, "B, H, L must be >= 1 (got %d, %d, %d)", B, H, L);
   FC_REQUIRE(L <= kMaxSteps, FC_EUNSUPPORTED, "L = %d > 2^30", L);
+  FC_REQUIRE(H <= kMaxChannels, FC_EUNSUPPORTED, "H = %d > 2^30", H);
   // grids count blocks of up to 1024 steps of a row
   FC_REQUIRE((double)B * H * (((double)L + 1023) / 1024) < 2147483647.0, FC_EUNSUPPORTED,
              "B * H * ceil(L / 1024) must be below 2^31");

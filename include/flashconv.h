@@ -323,7 +323,7 @@ FC_API fc_status h3_mixer_decode_step(const void* q, const void* k, const void* 
  *    (other streams, graphs replayed side by side) need one each.
  *  - Results do not depend on the order in which blocks run: the same call
  *    gives the same bits.
- *  - Limits: 1 <= L <= 2^30, B * H * ceil(L / 1024) < 2^31, B * G * N * L <
+ *  - Limits: 1 <= L <= 2^30, H <= 2^30, B * H * ceil(L / 1024) < 2^31, B * G * N * L <
  *    2^37, N <= 256, K <= 8.  Workspace sizes are those of the current device. */
 
 /* short_conv_fwd -- short causal convolution by channels with bias and SiLU,

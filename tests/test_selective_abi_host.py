@@ -223,3 +223,15 @@ def test_wrappers_refuse_tensors_of_another_device():
     with pytest.raises(ValueError, match="CUDA"):
         api._device(meta)
     assert api._device(Fake("cuda:1"), None, Fake("cuda:1")) == torch.device("cuda:1")
+
+
+@pytest.mark.parametrize("H", [(1 << 30) + 1, (1 << 31) - 2])
+@pytest.mark.parametrize("call,kw", [
+    (conv_fwd, {"L": 1}), (conv_bwd, {"L": 1}), (conv_step, {"S": 1}), (scan_fwd, {"L": 1, "G": 1}),
+    (scan_bwd, {"L": 1, "G": 1}), (scan_step, {"S": 1, "G": 1}),
+])
+def test_more_channels_than_an_int_index_holds(call, kw, H):
+    # a block's last channel lies up to a block past H; y is bad too, so nothing can launch
+    kw = dict(kw, B=1, H=H, **({"dx": None} if call is conv_bwd else {"du": None} if call is scan_bwd else {"y": None}))
+    assert call(**kw) == EUNSUP
+    assert "H = " in _err() and "2^30" in _err()
