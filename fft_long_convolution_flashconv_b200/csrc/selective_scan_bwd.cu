@@ -7,9 +7,9 @@
 //   dA_n = sum_{b,t} dt g_n a_n x_n[t-1],  dD = sum dyp u,  ddt_bias = sum ddelta
 //   dB_n[t] = sum_h g_n dt u,  dC_n[t] = sum_h dyp x_n,  dz = dy y silu'(z)
 //
-// Measured: 37 instructions and 62 cycles a warp, state and step, bound by their
-// issue; 0.91 ms for 4 x 1024 channels of 8192 steps, 16 states, bf16, and 0.17 ms
-// for the states entering its segments.
+// Measured: 35 instructions and 56 cycles a warp, state and step, bound by their
+// issue (62% of its slots); 217 us for 4 x 1024 channels of 2048 steps, 16 states,
+// bf16.
 //
 // A lane holds eight steps of one channel; eight lanes are a channel's 64-step
 // block, a warp takes four channels and walks through the blocks from the last
@@ -23,8 +23,9 @@
 // so results do not change from run to run.  (Adding up the lanes by products with
 // ones on the tensor cores cost more instructions, most of them moves into operand
 // registers; two channels a lane would halve the shuffles but spill at the 168
-// registers that three blocks an SM leave: 1556 and 1799 us against 1537 for a
-// training step of 4 x 1024 channels of 8192 steps.)
+// registers that three blocks an SM leave, and gain nothing with two: 1556 to
+// 1799 us for a training step of 4 x 1024 channels of 8192 steps, when this form
+// took 1537.)
 #include "kernels.cuh"
 #include "scan.cuh"
 
