@@ -156,7 +156,10 @@ __global__ __launch_bounds__(kThreads, 4) void scan_ends_kernel(ScanArgs p, Segm
       const float o = BACK ? __shfl_up_sync(~0u, scan, d, TL) : __shfl_down_sync(~0u, scan, d, TL);
       if (BACK ? tl >= d : tl + d < TL) scan += o;
     }
-    const float off = edge + scan - sum;
+    // the lanes between this one and the edge: taken from the neighbour, since scan - sum would cancel away small
+    // distances behind one large step
+    const float ahead = BACK ? __shfl_up_sync(~0u, scan, 1, TL) : __shfl_down_sync(~0u, scan, 1, TL);
+    const float off = edge + (tl == (BACK ? 0 : TL - 1) ? 0.f : ahead);
     edge += __shfl_sync(~0u, scan, BACK ? TL - 1 : 0, TL);
 #pragma unroll
     for (int e = 0; e < PAIRS; ++e) S[e] = add2(S[e], both(off));
