@@ -90,6 +90,9 @@ __device__ __forceinline__ float2 cmul(float2 a, float2 b) {
 __device__ __forceinline__ float2 cconj(float2 a) { return make_float2(a.x, -a.y); }
 
 // ---- I/O element types --------------------------------------------------------------
+// ld reads through the read-only path where that is safe under a condition.  The headers' __ldg of a 16-bit type is an
+// assembly statement that is not volatile: the compiler may execute it ahead of the condition that guards it, and then
+// read past a tensor's end.  So 16-bit elements are read by plain loads (of restrict pointers: the same instruction).
 template <typename T> struct IO;
 template <> struct IO<float> {
   static __device__ __forceinline__ float ld(const float* p) { return __ldg(p); }
@@ -97,12 +100,12 @@ template <> struct IO<float> {
   static __device__ __forceinline__ void st(float* p, float v) { *p = v; }
 };
 template <> struct IO<__half> {
-  static __device__ __forceinline__ float ld(const __half* p) { return __half2float(__ldg(p)); }
+  static __device__ __forceinline__ float ld(const __half* p) { return __half2float(*p); }
   static __device__ __forceinline__ float ldplain(const __half* p) { return __half2float(*p); }
   static __device__ __forceinline__ void st(__half* p, float v) { *p = __float2half_rn(v); }
 };
 template <> struct IO<__nv_bfloat16> {
-  static __device__ __forceinline__ float ld(const __nv_bfloat16* p) { return __bfloat162float(__ldg(p)); }
+  static __device__ __forceinline__ float ld(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   static __device__ __forceinline__ float ldplain(const __nv_bfloat16* p) { return __bfloat162float(*p); }
   static __device__ __forceinline__ void st(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 };

@@ -104,7 +104,7 @@ __device__ __forceinline__ void fft_inv(float2* v, float2* buf, int tid, const f
 }
 
 // Two rows' inputs at one stage-0 position, kept in registers from the load
-// (prefetch) until the D*u term of the output.
+// (prefetch) until the D*u term of the output.  Called under the row's bound, so 16-bit loads are plain (see IO).
 template <typename T> struct UPair;
 template <> struct UPair<float> {
   float2 v;
@@ -118,7 +118,7 @@ template <> struct UPair<float> {
 template <> struct UPair<__half> {
   __half2 v;
   __device__ __forceinline__ void load(const __half* a, const __half* b, bool hb) {
-    v = __halves2half2(__ldg(a), hb ? __ldg(b) : __float2half_rn(0.f));
+    v = __halves2half2(*a, hb ? *b : __float2half_rn(0.f));
   }
   __device__ __forceinline__ float2 get() const { return __half22float2(v); }
   __device__ __forceinline__ void zero() { v = __float2half2_rn(0.f); }
@@ -126,7 +126,7 @@ template <> struct UPair<__half> {
 template <> struct UPair<__nv_bfloat16> {
   __nv_bfloat162 v;
   __device__ __forceinline__ void load(const __nv_bfloat16* a, const __nv_bfloat16* b, bool hb) {
-    v = __halves2bfloat162(__ldg(a), hb ? __ldg(b) : __float2bfloat16_rn(0.f));
+    v = __halves2bfloat162(*a, hb ? *b : __float2bfloat16_rn(0.f));
   }
   __device__ __forceinline__ float2 get() const { return __bfloat1622float2(v); }
   __device__ __forceinline__ void zero() { v = __float2bfloat162_rn(0.f); }
