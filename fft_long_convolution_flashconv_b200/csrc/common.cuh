@@ -9,6 +9,8 @@
 
 #include <atomic>
 
+#include "optin.h"
+
 namespace fc {
 
 // Diagonal-SSM parameters for kernels that generate their filter (dt == nullptr: none).
@@ -42,23 +44,14 @@ inline int num_sms() {
   return n;
 }
 
-// Opt the kernel Kern in to `bytes` of dynamic shared memory once per device
-// (one cache per kernel instantiation; requests are monotone per kernel).
+// Opt the kernel Kern in to `bytes` of dynamic shared memory, where no launch on
+// this device has asked for as much yet (one limit per kernel instantiation).
 template <auto Kern>
 cudaError_t smem_optin(size_t bytes) {
-  static std::atomic<unsigned long long> done{0};
-  static std::atomic<size_t> max_bytes[64];
-  const int d = current_device();
-  const bool cacheable = d >= 0 && d < 64;
-  if (cacheable && (done.load(std::memory_order_acquire) >> d & 1ull) &&
-      max_bytes[d].load(std::memory_order_relaxed) >= bytes)
-    return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e == cudaSuccess && cacheable) {
-    max_bytes[d].store(bytes, std::memory_order_relaxed);
-    done.fetch_or(1ull << d, std::memory_order_release);
-  }
-  return e;
+  static RaisedLimit limit;
+  return limit.raise(current_device(), bytes, [](size_t n) {
+    return cudaFuncSetAttribute(Kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)n);
+  });
 }
 
 // Debug-build bounds checks (-DFC_CHECK): a failed check records
