@@ -296,8 +296,10 @@ def _device(first: torch.Tensor, *others) -> torch.device:
     return dev
 
 
-_current_device = torch._C._cuda_getDevice
-_raw_stream = torch._C._cuda_getCurrentRawStream
+# What torch.cuda.current_device() and current_stream() ask, without their checks; a torch built
+# without CUDA has neither, and no tensor that gets past _device().
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _call(dev: torch.device, name: str, *args) -> None:
