@@ -495,10 +495,29 @@ size_t rows_end(const fc::Rows& r, int B, int G, int R, int len) {
   return (size_t)((B - 1) * r.bs + (G - 1) * r.gs + (R - 1) * r.rs + len);
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const char* x = (const char*)a;
-  const char* y = (const char*)b;
-  return a && b && na && nb && x < y + nb && y < x + na;
+// An array of a call: `bytes` from its first element to its last (p null or 0 bytes: absent).
+struct Span {
+  const char* name;
+  const void* p;
+  size_t bytes;
+};
+
+bool overlap(const Span& a, const Span& b) {
+  const char* x = (const char*)a.p;
+  const char* y = (const char*)b.p;
+  return x && y && a.bytes && b.bytes && x < y + b.bytes && y < x + a.bytes;
+}
+
+// No output (the workspace counts as one) may touch an input or another output.
+extern "C++" template <int NI, int NO>
+fc_status check_overlaps(const Span (&in)[NI], const Span (&out)[NO], const char* outputs) {
+  for (int i = 0; i < NO; ++i) {
+    for (const Span& s : in) FC_REQUIRE(!overlap(s, out[i]), FC_EINVAL, "%s overlaps an input (%s)", out[i].name, s.name);
+    for (int j = 0; j < i; ++j)
+      FC_REQUIRE(!overlap(out[j], out[i]), FC_EINVAL, "two %s, %s and %s: one overlaps the other", outputs,
+                 out[j].name, out[i].name);
+  }
+  return FC_OK;
 }
 
 fc_status check_sizes(int B, int H, int L, int dtype) {
@@ -545,11 +564,11 @@ FC_API fc_status short_conv_fwd(const void* x, const float* w, const float* bias
              "lengths and states must be aligned to their elements");
   fc::Rows xr;
   FC_REQUIRE(rows_of(&xr, x, strides, false, B, 1, H, L, dtype), FC_EINVAL, "strides must be >= 0 and in range");
-  const size_t xe = rows_end(xr, B, 1, H, L) * e, ye = (size_t)B * H * L * e;
-  FC_REQUIRE(!overlap(x, xe, y, ye) && !overlap(state_in, tail, y, ye), FC_EINVAL, "y overlaps an input");
-  FC_REQUIRE(!overlap(x, xe, state_out, tail) && !overlap(y, ye, state_out, tail) &&
-                 !overlap(state_in, tail, state_out, tail),
-             FC_EINVAL, "state_out overlaps another array");
+  const size_t he = (size_t)H * 4;
+  const Span in[] = {{"x", x, rows_end(xr, B, 1, H, L) * e}, {"state_in", state_in, tail}, {"w", w, he * K},
+                     {"bias", bias, he}, {"lengths", lengths, (size_t)B * 4}};
+  const Span out[] = {{"y", y, (size_t)B * H * L * e}, {"state_out", state_out, tail}};
+  if ((s = check_overlaps(in, out, "outputs")) != FC_OK) return s;
   return cuda_status(fc::launch_short_conv(xr, w, bias, y, B, H, L, K, silu, lengths, K > 1 ? state_in : nullptr,
                                            K > 1 ? state_out : nullptr, L % (16 / (int)e) == 0, dtype,
                                            (cudaStream_t)stream),
@@ -578,17 +597,15 @@ FC_API fc_status short_conv_bwd(const void* dy, const void* x, const float* w, c
   FC_REQUIRE(rows_of(&gr, dy, strides, false, B, 1, H, L, dtype) &&
                  rows_of(&xr, x, strides ? strides + 2 : nullptr, false, B, 1, H, L, dtype),
              FC_EINVAL, "strides must be >= 0 and in range");
-  const size_t xe = rows_end(xr, B, 1, H, L) * e, ge = rows_end(gr, B, 1, H, L) * e, oe = (size_t)B * H * L * e;
-  FC_REQUIRE(!overlap(x, xe, dx, oe) && !overlap(dy, ge, dx, oe) && !overlap(state_in, tail, dx, oe) &&
-                 !overlap(dstate_out, tail, dx, oe),
-             FC_EINVAL, "dx overlaps an input");
-  FC_REQUIRE(!overlap(x, xe, dstate_in, tail) && !overlap(dy, ge, dstate_in, tail) &&
-                 !overlap(dx, oe, dstate_in, tail) && !overlap(state_in, tail, dstate_in, tail) &&
-                 !overlap(dstate_out, tail, dstate_in, tail),
-             FC_EINVAL, "dstate_in overlaps another array");
-  const size_t need = short_conv_bwd_workspace(B, H, L, K);
+  const size_t need = short_conv_bwd_workspace(B, H, L, K), he = (size_t)H * 4;
   FC_REQUIRE(workspace && aligned(workspace, 256), FC_EINVAL, "workspace must be non-null and 256-byte aligned");
   FC_REQUIRE(ws_bytes >= need, FC_EINVAL, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  const Span in[] = {{"dy", dy, rows_end(gr, B, 1, H, L) * e}, {"x", x, rows_end(xr, B, 1, H, L) * e},
+                     {"state_in", state_in, tail}, {"dstate_out", dstate_out, tail}, {"w", w, he * K},
+                     {"bias", bias, he}, {"lengths", lengths, (size_t)B * 4}};
+  const Span out[] = {{"dx", dx, (size_t)B * H * L * e}, {"dstate_in", dstate_in, tail}, {"dw", dw, he * K},
+                      {"dbias", dbias, he}, {"workspace", workspace, need}};
+  if ((s = check_overlaps(in, out, "gradients")) != FC_OK) return s;
   return cuda_status(
       fc::launch_short_conv_bwd(gr, xr, w, bias, dx, dw, dbias, B, H, L, K, silu, lengths, K > 1 ? state_in : nullptr,
                                 K > 1 ? dstate_out : nullptr, K > 1 ? dstate_in : nullptr, (float*)workspace,
@@ -607,10 +624,11 @@ FC_API fc_status short_conv_step(const void* x, void* state, const float* w, con
   FC_REQUIRE(y && aligned(y, e), FC_EINVAL, "y must be non-null and aligned to its elements");
   FC_REQUIRE(K == 1 || (state && aligned(state, e)), FC_EINVAL, "state must be non-null and aligned to its elements");
   FC_REQUIRE(x_stride >= 0 && x_stride <= (1LL << 60) / B, FC_EINVAL, "x_stride must be >= 0 and in range");
-  const size_t xe = (size_t)((B - 1) * x_stride + H) * e, ye = (size_t)B * H * e;
-  FC_REQUIRE(!overlap(x, xe, y, ye), FC_EINVAL, "x and y overlap");
-  FC_REQUIRE(K == 1 || (!overlap(x, xe, state, pool) && !overlap(y, ye, state, pool)), FC_EINVAL,
-             "state overlaps x or y");
+  const size_t he = (size_t)H * 4;
+  const Span in[] = {{"x", x, (size_t)((B - 1) * x_stride + H) * e}, {"w", w, he * K}, {"bias", bias, he},
+                     {"slots", slots, (size_t)B * 4}};
+  const Span out[] = {{"y", y, (size_t)B * H * e}, {"state", state, pool}};
+  if ((s = check_overlaps(in, out, "outputs")) != FC_OK) return s;
   return cuda_status(fc::launch_short_conv_step(x, x_stride, state, w, bias, y, B, H, K, silu, slots, S, dtype,
                                                 (cudaStream_t)stream),
                      "short_conv_step launch");
@@ -653,13 +671,20 @@ static fc_status scan_args(fc::ScanArgs* p, const void* u, const void* delta, co
   return FC_OK;
 }
 
-// Whether [q, q + bytes) touches one of the scan's B x H x L or B x G x N x L inputs.
-static bool hits_scan_input(const fc::ScanArgs& p, size_t e, const void* q, size_t bytes) {
-  return overlap(p.u.p, rows_end(p.u, p.B, 1, p.H, p.L) * e, q, bytes) ||
-         overlap(p.delta.p, rows_end(p.delta, p.B, 1, p.H, p.L) * e, q, bytes) ||
-         overlap(p.z.p, rows_end(p.z, p.B, 1, p.H, p.L) * e, q, bytes) ||
-         overlap(p.Bt.p, rows_end(p.Bt, p.B, p.G, p.N, p.L) * e, q, bytes) ||
-         overlap(p.Ct.p, rows_end(p.Ct, p.B, p.G, p.N, p.L) * e, q, bytes);
+// The inputs that the scan's calls share, as the first kScanInputs of a list.
+constexpr int kScanInputs = 9;
+static void scan_inputs(const fc::ScanArgs& p, size_t e, Span* in) {
+  const size_t he = (size_t)p.H * 4;
+  const Span all[kScanInputs] = {{"u", p.u.p, rows_end(p.u, p.B, 1, p.H, p.L) * e},
+                                 {"delta", p.delta.p, rows_end(p.delta, p.B, 1, p.H, p.L) * e},
+                                 {"z", p.z.p, rows_end(p.z, p.B, 1, p.H, p.L) * e},
+                                 {"Bt", p.Bt.p, rows_end(p.Bt, p.B, p.G, p.N, p.L) * e},
+                                 {"Ct", p.Ct.p, rows_end(p.Ct, p.B, p.G, p.N, p.L) * e},
+                                 {"A", p.A, he * p.N},
+                                 {"D", p.D, he},
+                                 {"dt_bias", p.dt_bias, he},
+                                 {"lengths", p.lengths, (size_t)p.B * 4}};
+  for (int i = 0; i < kScanInputs; ++i) in[i] = all[i];
 }
 
 FC_API size_t selective_scan_ckpt_bytes(int B, int H, int L, int N) {
@@ -685,20 +710,18 @@ FC_API fc_status selective_scan_fwd(const void* u, const void* delta, const floa
   FC_REQUIRE(aligned(state_in, 4) && aligned(state_out, 4) && aligned(ckpt, 4), FC_EINVAL,
              "states must be 4-byte aligned");
   p.state_in = state_in;
-  const size_t e = dtype_size(dtype), ye = (size_t)B * H * L * e, se = (size_t)B * H * N * 4;
-  const size_t ce = selective_scan_ckpt_bytes(B, H, L, N);
-  FC_REQUIRE(!hits_scan_input(p, e, y, ye) && !overlap(state_in, se, y, ye), FC_EINVAL, "y overlaps an input");
-  FC_REQUIRE(!hits_scan_input(p, e, state_out, se) && !overlap(y, ye, state_out, se) &&
-                 !overlap(state_in, se, state_out, se),
-             FC_EINVAL, "state_out overlaps another array");
-  FC_REQUIRE(!hits_scan_input(p, e, ckpt, ce) && !overlap(y, ye, ckpt, ce) && !overlap(state_in, se, ckpt, ce) &&
-                 !overlap(state_out, se, ckpt, ce),
-             FC_EINVAL, "ckpt overlaps another array");
   const size_t need = selective_scan_workspace(B, H, L, N, G);
   if (need) {
     FC_REQUIRE(workspace && aligned(workspace, 256), FC_EINVAL, "workspace must be non-null and 256-byte aligned");
     FC_REQUIRE(ws_bytes >= need, FC_EINVAL, "workspace too small: %zu < %zu bytes", ws_bytes, need);
   }
+  const size_t e = dtype_size(dtype), se = (size_t)B * H * N * 4;
+  Span in[kScanInputs + 1];
+  scan_inputs(p, e, in);
+  in[kScanInputs] = {"state_in", state_in, se};
+  const Span out[] = {{"y", y, (size_t)B * H * L * e}, {"state_out", state_out, se},
+                      {"ckpt", ckpt, selective_scan_ckpt_bytes(B, H, L, N)}, {"workspace", workspace, need}};
+  if ((s = check_overlaps(in, out, "outputs")) != FC_OK) return s;
   return cuda_status(fc::launch_selective_scan(p, y, state_out, ckpt, workspace, dtype, (cudaStream_t)stream),
                      "selective_scan_fwd launch");
 }
@@ -728,17 +751,20 @@ FC_API fc_status selective_scan_bwd(const void* dy, const void* u, const void* d
                  aligned(dD, 4) && aligned(ddt_bias, 4) && aligned(dstate_out, 4) && aligned(dstate_in, 4),
              FC_EINVAL, "arrays must be aligned to their elements");
   FC_REQUIRE(rows_of(&p.dy, dy, strides, false, B, 1, H, L, dtype), FC_EINVAL, "strides must be >= 0 and in range");
-  const size_t ge = rows_end(p.dy, B, 1, H, L) * e, oe = (size_t)B * H * L * e, be = (size_t)B * G * N * L * e;
-  const struct { const void* q; size_t n; } out[] = {{du, oe}, {ddelta, oe}, {dz, oe}, {dB, be}, {dC, be}};
-  for (int i = 0; i < 5; ++i) {
-    FC_REQUIRE(!hits_scan_input(p, e, out[i].q, out[i].n) && !overlap(dy, ge, out[i].q, out[i].n), FC_EINVAL,
-               "a gradient overlaps an input");
-    for (int j = 0; j < i; ++j)
-      FC_REQUIRE(!overlap(out[j].q, out[j].n, out[i].q, out[i].n), FC_EINVAL, "two gradients overlap");
-  }
   const size_t need = selective_scan_bwd_workspace(B, H, L, N, G);
   FC_REQUIRE(workspace && aligned(workspace, 256), FC_EINVAL, "workspace must be non-null and 256-byte aligned");
   FC_REQUIRE(ws_bytes >= need, FC_EINVAL, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  const size_t oe = (size_t)B * H * L * e, be = (size_t)B * G * N * L * e, se = (size_t)B * H * N * 4;
+  const size_t he = (size_t)H * 4;
+  Span in[kScanInputs + 3];
+  scan_inputs(p, e, in);
+  in[kScanInputs] = {"dy", dy, rows_end(p.dy, B, 1, H, L) * e};
+  in[kScanInputs + 1] = {"ckpt", ckpt, selective_scan_ckpt_bytes(B, H, L, N)};
+  in[kScanInputs + 2] = {"dstate_out", dstate_out, se};
+  const Span out[] = {{"du", du, oe}, {"ddelta", ddelta, oe}, {"dz", dz, oe}, {"dB", dB, be}, {"dC", dC, be},
+                      {"dA", dA, he * N}, {"dD", dD, he}, {"ddt_bias", ddt_bias, he}, {"dstate_in", dstate_in, se},
+                      {"workspace", workspace, need}};
+  if ((s = check_overlaps(in, out, "gradients")) != FC_OK) return s;
   return cuda_status(fc::launch_selective_scan_bwd(p, ckpt, du, ddelta, dA, dB, dC, dD, ddt_bias, dz, dstate_out,
                                                    dstate_in, workspace, dtype, (cudaStream_t)stream),
                      "selective_scan_bwd launch");
@@ -754,12 +780,14 @@ FC_API fc_status selective_scan_step(const void* u, const void* delta, const flo
       scan_args(&p, u, delta, A, Bt, Ct, D, dt_bias, z, B, H, 1, N, G, softplus, nullptr, strides, dtype);
   if (s != FC_OK) return s;
   if ((s = check_step(B, S, slots)) != FC_OK) return s;
-  const size_t e = dtype_size(dtype), ye = (size_t)B * H * e, pool = (size_t)S * H * N * 4;
+  const size_t e = dtype_size(dtype);
   FC_REQUIRE(y && aligned(y, e), FC_EINVAL, "y must be non-null and aligned to its elements");
   FC_REQUIRE(state && aligned(state, 4), FC_EINVAL, "state must be non-null and 4-byte aligned");
-  FC_REQUIRE(!hits_scan_input(p, e, y, ye), FC_EINVAL, "y overlaps an input");
-  FC_REQUIRE(!hits_scan_input(p, e, state, pool) && !overlap(y, ye, state, pool), FC_EINVAL,
-             "state overlaps another array");
+  Span in[kScanInputs + 1];
+  scan_inputs(p, e, in);
+  in[kScanInputs] = {"slots", slots, (size_t)B * 4};
+  const Span out[] = {{"state", state, (size_t)S * H * N * 4}, {"y", y, (size_t)B * H * e}};
+  if ((s = check_overlaps(in, out, "outputs")) != FC_OK) return s;
   return cuda_status(fc::launch_selective_scan_step(p, state, y, slots, S, dtype, (cudaStream_t)stream),
                      "selective_scan_step launch");
 }
@@ -793,7 +821,9 @@ FC_API fc_status group_norm_act_fwd(const void* x, const float* weight, const fl
   if (s != FC_OK) return s;
   const size_t e = dtype_size(dtype), n = (size_t)B * L * C * e;
   FC_REQUIRE(y && aligned(y, 16), FC_EINVAL, "y must be non-null and 16-byte aligned");
-  FC_REQUIRE(!overlap(x, n, y, n) && !overlap(gate, n, y, n), FC_EINVAL, "y overlaps an input");
+  const Span in[] = {{"x", x, n}, {"gate", gate, n}, {"weight", weight, (size_t)C * 4}, {"bias", bias, (size_t)C * 4}};
+  const Span out[] = {{"y", y, n}};
+  if ((s = check_overlaps(in, out, "outputs")) != FC_OK) return s;
   return cuda_status(fc::launch_group_norm(x, weight, bias, gate, y, B, L, C, G, eps, channel_major,
                                            norm_vec(L, C, G, channel_major, e), dtype, (cudaStream_t)stream),
                      "group_norm_act_fwd launch");
@@ -816,13 +846,14 @@ FC_API fc_status group_norm_act_bwd(const void* dy, const void* x, const float* 
              "dy and dx must be non-null, dy, dx and dgate 16-byte aligned");
   FC_REQUIRE(aligned(dweight, 4) && aligned(dbias, 4), FC_EINVAL, "dweight and dbias must be 4-byte aligned");
   FC_REQUIRE((gate == nullptr) == (dgate == nullptr), FC_EINVAL, "gate and dgate must both be given or both be null");
-  const void* in[] = {dy, x, gate};
-  for (const void* q : in)
-    FC_REQUIRE(!overlap(q, n, dx, n) && !overlap(q, n, dgate, n), FC_EINVAL, "a gradient overlaps an input");
-  FC_REQUIRE(!overlap(dx, n, dgate, n), FC_EINVAL, "dx and dgate overlap");
   const size_t need = group_norm_act_bwd_workspace(B, L, C, G, channel_major);
   FC_REQUIRE(workspace && aligned(workspace, 256), FC_EINVAL, "workspace must be non-null and 256-byte aligned");
   FC_REQUIRE(ws_bytes >= need, FC_EINVAL, "workspace too small: %zu < %zu bytes", ws_bytes, need);
+  const size_t ce = (size_t)C * 4;
+  const Span in[] = {{"dy", dy, n}, {"x", x, n}, {"gate", gate, n}, {"weight", weight, ce}, {"bias", bias, ce}};
+  const Span out[] = {{"dx", dx, n}, {"dgate", dgate, n}, {"dweight", dweight, ce}, {"dbias", dbias, ce},
+                      {"workspace", workspace, need}};
+  if ((s = check_overlaps(in, out, "gradients")) != FC_OK) return s;
   return cuda_status(fc::launch_group_norm_bwd(dy, x, weight, bias, gate, dx, dweight, dbias, dgate, B, L, C, G, eps,
                                                channel_major, norm_vec(L, C, G, channel_major, e), (float*)workspace,
                                                dtype, (cudaStream_t)stream),

@@ -310,7 +310,8 @@ FC_API fc_status h3_mixer_decode_step(const void* q, const void* k, const void* 
  *    entries that each call names, batch first), NULL when every input is
  *    contiguous.  Inputs are aligned to their elements; rows on 16-byte
  *    boundaries run faster.  Outputs are contiguous and 16-byte aligned where
- *    they are sequences; no output overlaps an input or another output.
+ *    they are sequences; no output, state or workspace overlaps an input
+ *    (strided ones count from their first element to their last) or another output.
  *  - lengths: B int32 on the device, or NULL (every row has L steps).  A value
  *    outside [0, L] counts as the nearer end.  Outputs and gradients at t >=
  *    lengths[b] are zeros, inputs there are never used (whatever they hold),

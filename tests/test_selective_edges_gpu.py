@@ -46,3 +46,16 @@ def test_large_steps_among_small_ones_in_segments(B, H, L, N, dtype, sizes):
     for name, g in zip(GRADS, scan_bwd(c, c, args, ckpt)):
         if name != "ddt_bias":
             T.close(g, want[name], mag[name], 2 * k, name)
+
+
+def test_workspace_over_an_output_is_refused():
+    c = T.scan_case(1, 3, 1500, 4, 1, "f32", 2, ("D",))
+    a = [c[k].cuda() for k in ("u", "delta", "A", "Bt", "Ct", "D")]
+    need = api.selective_scan_workspace_bytes(1, 3, 1500, 4, 1)
+    assert need > 0
+    ws = torch.zeros(need + 3 * 1500 * 4, dtype=torch.uint8, device="cuda")
+    out = ws.view(torch.float32)[need // 4 - 4:][:3 * 1500].view(1, 3, 1500)  # begins inside the workspace
+    with pytest.raises(Exception, match="y and workspace: one overlaps the other"):
+        api.selective_scan_fwd(*a, workspace=ws, out=out)
+    out = ws.view(torch.float32)[need // 4:][:3 * 1500].view(1, 3, 1500)  # right behind what the call uses
+    assert torch.equal(api.selective_scan_fwd(*a, workspace=ws, out=out), api.selective_scan_fwd(*a))
