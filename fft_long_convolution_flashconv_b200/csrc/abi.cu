@@ -697,6 +697,11 @@ FC_API size_t selective_scan_workspace(int B, int H, int L, int N, int G) {
   return fc::selective_scan_workspace_bytes(B, H, L, N, G);
 }
 
+FC_TEST_API int fc_debug_scan_lane_steps(int B, int H, int L, int N, int G) {
+  if (B < 1 || H < 1 || L < 1 || N < 1 || G < 1 || H % G) return 0;
+  return fc::selective_scan_lane_steps(B, H, L, N, G);
+}
+
 FC_API fc_status selective_scan_fwd(const void* u, const void* delta, const float* A, const void* Bt, const void* Ct,
                                     const float* D, const float* dt_bias, const void* z, void* y, int B, int H, int L,
                                     int N, int G, int softplus, const int* lengths, const long long* strides,

@@ -131,6 +131,7 @@ cudaError_t launch_short_conv_step(const void* x, long long xs, void* state, con
 // Selective scan (selective_scan.cu, selective_scan_bwd.cu); scan.cuh has
 // ScanArgs.  ckpt: B x H x ceil(L / 64) x N states entering the 64-step blocks.
 size_t selective_scan_workspace_bytes(int B, int H, int L, int N, int G);
+int selective_scan_lane_steps(int B, int H, int L, int N, int G);  // 8 or 16: which form the plan takes
 cudaError_t launch_selective_scan(const ScanArgs& p, void* y, float* state_out, float* ckpt, void* workspace, int dtype,
                                   cudaStream_t st);
 cudaError_t launch_selective_scan_step(const ScanArgs& p, float* state, void* y, const int* slots, int S, int dtype,

@@ -580,6 +580,8 @@ cudaError_t step(const ScanArgs& p, float* state, void* y, const int* slots, int
 
 }  // namespace
 
+int selective_scan_lane_steps(int B, int H, int L, int N, int G) { return plan(B, H, L, N, G).tpl; }
+
 size_t selective_scan_workspace_bytes(int B, int H, int L, int N, int G) {
   return segments_bytes(plan(B, H, L, N, G).sg, B, H, N);
 }

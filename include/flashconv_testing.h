@@ -46,6 +46,11 @@ FC_TEST_API int fc_selftest_umma_tmem_a(const void* A, const void* B, float* D, 
  * operation; the GPU tests assert that it stays 0. */
 FC_TEST_API unsigned int fc_debug_tc_timeouts(void);
 
+/* Steps of a channel that a lane of selective_scan_fwd's kernel holds for these
+ * sizes on the current device (8 or 16; 0 for sizes that the call refuses), so
+ * that the tests can tell which form of the kernel they run. */
+FC_TEST_API int fc_debug_scan_lane_steps(int B, int H, int L, int N, int G);
+
 #ifdef __cplusplus
 }
 #endif

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import test_selective_gpu as T
-from fft_long_convolution_flashconv_b200 import api
+from fft_long_convolution_flashconv_b200 import _lib, api
 
 pytestmark = pytest.mark.gpu
 _cuda = T._cuda
@@ -59,3 +59,121 @@ def test_workspace_over_an_output_is_refused():
         api.selective_scan_fwd(*a, workspace=ws, out=out)
     out = ws.view(torch.float32)[need // 4:][:3 * 1500].view(1, 3, 1500)  # right behind what the call uses
     assert torch.equal(api.selective_scan_fwd(*a, workspace=ws, out=out), api.selective_scan_fwd(*a))
+
+
+# ------------------------------------------------------------------ sixteen steps a lane
+def scan_want_on_gpu(c):
+    """scan_want with its 64-bit steps on the GPU (some thousand channels)."""
+    with torch.device("cuda"):
+        want, mag = T.scan_want({k: v.cuda() if torch.is_tensor(v) else v for k, v in c.items()})
+    return ({k: v.detach().cpu() for k, v in d.items()} for d in (want, mag))
+
+
+@pytest.mark.parametrize("B,H,L,N,G,dtype,segments,view,opts", [
+    # rows on 16-byte boundaries; a last group of channels that is not full; two chunks of states
+    (5, 2000, 136, 16, 1, "f16", False, False, ("D", "bias", "gate", "state", "ragged")),
+    (4, 2404, 200, 20, 2, "bf16", False, False, ("D", "bias", "gate", "state", "ragged")),
+    (3, 3200, 200, 4, 1, "f32", False, False, ("D", "gate", "state", "ragged", "raw")),
+    # rows on two-byte boundaries: blocks inside the sequence load together
+    (5, 1920, 203, 16, 1, "f16", False, False, ("D", "bias", "gate", "state", "ragged")),
+    (2, 5000, 269, 33, 1, "bf16", False, False, ("bias", "state")),
+    # rows of both kinds, NaN around them, and fp32 rows on four-byte boundaries
+    (5, 1920, 200, 5, 1, "f16", False, True, ("D", "bias", "gate", "state", "ragged")),
+    (3, 3201, 150, 3, 3, "f32", False, True, ("D", "bias", "gate", "state", "ragged")),
+    # in segments, both kinds of rows
+    (1, 1600, 1504, 4, 1, "bf16", True, False, ("D", "bias", "gate", "state")),
+    (1, 1600, 1501, 4, 1, "f16", True, False, ("D", "bias", "gate", "state")),
+])
+def test_scan_of_sixteen_steps_a_lane(B, H, L, N, G, dtype, segments, view, opts):
+    """Batches that fill the GPU take the form with sixteen steps a lane; its kept states feed the backward pass."""
+    assert _lib.load().fc_debug_scan_lane_steps(B, H, L, N, G) == 16
+    assert (api.selective_scan_workspace_bytes(B, H, L, N, G) > 0) == segments
+    c = T.scan_case(B, H, L, N, G, dtype, L + N, opts)
+    if segments:
+        c["dt_bias"] = torch.full((H,), -7.0)  # decays to e^-1 and so over the row: segments matter to one another
+    want, mag = scan_want_on_gpu(c)
+    p = T.poison(c)
+    # Sums over a group's channels have up to 200 more roundings of 2^-24 than kappa's tens: 1.2e-5, where kappa's
+    # count of k 2^-21 for an error of k 2^-22 leaves L 2^-22 (3.2e-5 at 136).
+    args, (y, state, ckpt) = T.call_fwd(p, view=view, return_state=True, return_ckpt=True)
+    T.close(y, want["y"], mag["y"], T.kappa(L), "y")
+    T.close(state, want["state"], mag["state"], T.kappa(L), "state")
+    _, plain = T.call_fwd(p, view=view)  # without kept states: another kernel, the same arithmetic
+    assert torch.equal(plain, y)
+    for k, g in zip(GRADS, scan_bwd(c, p, args, ckpt)):
+        if g is None:
+            assert k not in want
+        else:
+            T.close(g, want[k], mag[k], T.kappa(L, True), k)
+
+
+# ------------------------------------------------------------------ short convolution of aligned rows
+@pytest.mark.parametrize("B,H,L,K,dtype,silu,bias,state,ragged", [
+    (3, 5, 1024, 4, "f16", True, True, True, False),   # one block of 32 threads a row, every vector inside
+    (5, 6, 1024, 4, "bf16", True, True, True, True),   # rows that end inside a thread's vectors
+    (2, 3, 4096, 8, "f16", True, True, True, False),
+    (2, 4, 5128, 3, "f32", True, False, True, True),   # the last block of a row is not full
+    (2, 3, 1024, 1, "f32", False, True, False, False),
+    (3, 2, 1040, 7, "bf16", False, True, True, True),
+    (2, 3, 2048, 2, "f16", True, True, True, False),
+    (1, 3, 8192, 5, "f32", True, True, True, False),
+    (2, 2, 4104, 6, "bf16", True, True, False, False),
+    (2, 600, 1024, 4, "f16", True, True, True, True),  # one part a channel, several items a thread
+])
+def test_short_conv_of_aligned_rows(B, H, L, K, dtype, silu, bias, state, ragged):
+    x, w, bi, past, dy, dso, n = T.conv_case(B, H, L, K, dtype, silu, bias, state, ragged, seed=L + K)
+    ns = [L if n is None else int(n[b]) for b in range(B)]
+    zeros = torch.zeros(B, H, K - 1, dtype=torch.float64)
+    dbl = lambda t: None if t is None else t.double()  # noqa: E731
+
+    def run(f):
+        """Outputs, states and gradients in 64 bits, of the formula (f = identity) or of its magnitudes (f = abs)."""
+        on = f is not torch.abs
+        X, W, P = (f(t.double()).requires_grad_() for t in (x, w, zeros if past is None else past))
+        bb = None if bi is None else f(bi.double()).requires_grad_()
+        rows = [T.conv_ref(X[b], W, bb, silu and on, P[b], ns[b]) for b in range(B)]
+        y, s = torch.stack([r[0] for r in rows]), torch.stack([r[1] for r in rows])
+        scale = 1 if on else (1 + y.detach()) * 1.1  # silu' < 1.1, and dc's own error is relative to |dy| (1 + M)
+        loss = (y * f(dbl(dy)) * scale).sum() + (s * f(dbl(dso))).sum()
+        leaves = [X, W, P] + ([] if bb is None else [bb])
+        g = torch.autograd.grad(loss, leaves, allow_unused=True)
+        g = [torch.zeros_like(a) if v is None else v for a, v in zip(leaves, g)]
+        return y.detach(), s.detach(), g + [None] * (4 - len(g))
+
+    want, wstate, grads = run(lambda t: t)
+    mag, _, mags = run(torch.abs)
+    for b in range(B):  # padding may hold anything
+        x[b, :, ns[b]:] = T.NAN
+        dy[b, :, ns[b]:] = T.NAN
+    kap = 64 * 2.0 ** -22
+    a = (x.cuda(), w.cuda(), T.cu(bi), silu, T.cu(past), T.cu(n))
+    y, s = api.short_conv_fwd(*a, return_state=True)
+    T.close(y, want, mag * (1 + mag), kap, "y")
+    assert torch.equal(s.cpu().double(), wstate)
+    dx, dw, db, dp = api.short_conv_bwd(dy.cuda(), *a, T.cu(dso), need_dstate_in=True)
+    for name, g, r, m, k in (("dx", dx, grads[0], mags[0], kap), ("dstate_in", dp, grads[2], mags[2], kap),
+                             ("dw", dw, grads[1], mags[1], kap + 512 * 2.0 ** -24),
+                             ("dbias", db, grads[3], mags[3], kap + 512 * 2.0 ** -24)):
+        assert (g is None) == (r is None)
+        if g is not None:
+            T.close(g, r, m, k, name)
+
+
+# ------------------------------------------------------------------ group norm
+@pytest.mark.parametrize("B,L,C,G,dtype,opts,cm", [
+    # groups of 513 to 1024 channels: four vectors a lane of one warp
+    (2, 37, 768, 1, "f16", ("w", "b", "gate"), False),
+    (1, 33, 1024, 1, "f32", ("w", "b", "gate"), False),
+    (3, 50, 1544, 2, "bf16", ("w", "b"), False),       # groups of 772
+    (2, 65, 1040, 2, "f16", ("w", "gate"), False),     # groups of 520
+    (1, 20, 519, 1, "f32", ("b", "gate"), False),
+    # more groups than the GPU holds: every thread takes several
+    (5, 1000, 640, 1, "f16", ("w", "b", "gate"), False),
+    (2, 12000, 64, 1, "f16", ("w", "b", "gate"), False),
+    (1, 3000, 384, 1, "bf16", ("w", "b"), False),
+    (1, 700, 1100, 1, "f32", ("w", "b", "gate"), False),
+    (2, 400, 2050, 1, "bf16", ("w", "b"), False),
+    (1, 80001, 32, 1, "f16", ("w", "b", "gate"), True),
+])
+def test_group_norm_of_wide_groups_and_many_tokens(B, L, C, G, dtype, opts, cm):
+    T.test_group_norm_act(B, L, C, G, dtype, opts, cm)
