@@ -608,7 +608,8 @@ def group_norm_act_fwd(x: torch.Tensor, groups: int, weight: Optional[torch.Tens
                        channel_major: bool = False, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """Group norm of every token on its own, with SiLU: y = silu(n), or n silu(gate),
     n = (x - mean) / sqrt(var + eps) weight + bias over a group's channels.  x, gate:
-    B x L x C, or B x C x L with channel_major; y: B x L x C."""
+    B x L x C, or B x C x L with channel_major; y: B x L x C.  There is no `lengths`:
+    padding is normalised too (zeros give silu(bias))."""
     B, L, C = _norm_inputs(x, groups, weight, bias, gate, channel_major)
     _dense(out, "out", (B, L, C), x.dtype)
     dev = _device(x, weight, bias, gate, out)
@@ -627,7 +628,8 @@ def group_norm_act_bwd(dy: torch.Tensor, x: torch.Tensor, groups: int, weight: O
                        bias: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None, eps: float = 1e-5,
                        channel_major: bool = False, workspace: Optional[torch.Tensor] = None):
     """Gradients of group_norm_act_fwd given dy (B x L x C): (dx, dweight, dbias,
-    dgate), dx and dgate in x's layout (dweight, dbias, dgate: None where the input is)."""
+    dgate), dx and dgate in x's layout (dweight, dbias, dgate: None where the input is).
+    Tokens behind a padded row's end count in dweight and dbias unless their dy is zero."""
     B, L, C = _norm_inputs(x, groups, weight, bias, gate, channel_major)
     _dense(dy, "dy", (B, L, C), x.dtype)
     dev = _device(x, dy, weight, bias, gate)

@@ -324,6 +324,9 @@ FC_API fc_status h3_mixer_decode_step(const void* q, const void* k, const void* 
  *    (other streams, graphs replayed side by side) need one each.
  *  - Results do not depend on the order in which blocks run: the same call
  *    gives the same bits.
+ *  - Inputs may be parts of a wider tensor (the halves of a projection), outputs
+ *    and gradients are whole: joining the gradients of such halves for the
+ *    projection's own backward costs a read and a write of each.
  *  - Limits: 1 <= L <= 2^30, H <= 2^30, B * H * ceil(L / 1024) < 2^31, B * G * N * L <
  *    2^37, N <= 256, K <= 8.  Workspace sizes are those of the current device. */
 
@@ -372,6 +375,9 @@ FC_API fc_status short_conv_step(const void* x, void* state, const float* w, con
  * and then it may be NULL, where the batch and channels fill the GPU; long
  * sequences of few channels are cut into segments, whose entering states are
  * found in a first pass).
+ * A dt may have either sign, but decays are multiplied up over 64 steps, and over
+ * a segment where there are any: where states grow, exp(A times the sum of dt)
+ * over those has to stay below 2^127 (with A <= 0 and dt >= 0 it always does).
  * Precision: float32 state and arithmetic (exponentials by the special
  * function unit, relative error about 2^-22), y rounded once. */
 FC_API size_t selective_scan_ckpt_bytes(int B, int H, int L, int N);
@@ -392,7 +398,9 @@ FC_API fc_status selective_scan_fwd(const void* u, const void* delta, const floa
  * du, ddelta, dz: B x H x L, dB, dC: B x G x N x L in `dtype`; dA: H x N
  * floats; dD, ddt_bias: H floats or NULL; dz given where z is; dstate_in: B x
  * H x N floats or NULL.  strides: dy batch, row, then as selective_scan_fwd
- * (14).  workspace: selective_scan_bwd_workspace(...) bytes, 256-byte aligned.
+ * (14).  workspace: selective_scan_bwd_workspace(...) bytes, 256-byte aligned;
+ * most of it are float32 parts of dB and dC for every 16 channels of a group,
+ * B * H * L * N / 2 bytes (four times u's in 16 bits, at 16 states).
  * Precision: float32 states, sums and arithmetic. */
 FC_API size_t selective_scan_bwd_workspace(int B, int H, int L, int N, int G);
 FC_API fc_status selective_scan_bwd(const void* dy, const void* u, const void* delta, const float* A, const void* Bt,
@@ -419,7 +427,10 @@ FC_API fc_status selective_scan_step(const void* u, const void* delta, const flo
  * (selective_scan_fwd's output); y: B x L x C; weight, bias: C floats or NULL
  * (1, 0).  All contiguous and 16-byte aligned.  Limits: L <= 2^30, C <= 2^28,
  * C / G <= 8192, G <= 65535, B * L * G < 2^31, eps > 0.  Precision: float32 (mean first, then the
- * squares around it), y rounded once. */
+ * squares around it), y rounded once.
+ * There is no `lengths`: every token is normalised.  Behind a padded row's end,
+ * where the other calls write zeros, a group of zeros gives silu(bias), or bias
+ * silu(gate), and such tokens count in dweight and dbias unless their dy is zero. */
 FC_API fc_status group_norm_act_fwd(const void* x, const float* weight, const float* bias, const void* gate, void* y,
                                     int B, int L, int C, int G, float eps, int channel_major, fc_dtype dtype,
                                     void* stream);

@@ -48,6 +48,24 @@ def test_large_steps_among_small_ones_in_segments(B, H, L, N, dtype, sizes):
             T.close(g, want[name], mag[name], 2 * k, name)
 
 
+@pytest.mark.parametrize("L", [90, 1500])
+def test_growing_states(L):
+    """A above zero: states that grow by up to e^35 in one piece and in segments."""
+    assert (api.selective_scan_workspace_bytes(1, 3, L, 4, 1) > 0) == (L == 1500)
+    c = T.scan_case(1, 3, L, 4, 1, "f32", 41, ("D", "gate", "state", "raw"))
+    rng = np.random.default_rng(3)
+    c["A"] = torch.tensor(rng.uniform(0.05, 0.5, (3, 4)), dtype=torch.float32)
+    c["delta"] = torch.tensor(rng.uniform(0.001, 70 / L, (1, 3, L)), dtype=torch.float32)  # sum dt A <= 35
+    want, mag = T.scan_want(c)
+    args, (y, state, ckpt) = T.call_fwd(c, return_state=True, return_ckpt=True)
+    # |sum dt A| <= 35 over the row instead of 32: 3 * 2^-21 more, within kappa's 96 * 2^-21 of slack
+    T.close(y, want["y"], mag["y"], T.kappa(L), "y")
+    T.close(state, want["state"], mag["state"], T.kappa(L), "state")
+    for name, g in zip(GRADS, scan_bwd(c, c, args, ckpt)):
+        if name != "ddt_bias":
+            T.close(g, want[name], mag[name], T.kappa(L, True), name)
+
+
 def test_workspace_over_an_output_is_refused():
     c = T.scan_case(1, 3, 1500, 4, 1, "f32", 2, ("D",))
     a = [c[k].cuda() for k in ("u", "delta", "A", "Bt", "Ct", "D")]
