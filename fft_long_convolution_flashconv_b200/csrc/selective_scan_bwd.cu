@@ -8,7 +8,7 @@
 //   dB_n[t] = sum_h g_n dt u,  dC_n[t] = sum_h dyp x_n,  dz = dy y silu'(z)
 //
 // Measured: 35 instructions and 56 cycles a warp, state and step, bound by their
-// issue (62% of its slots); 217 us for 4 x 1024 channels of 2048 steps, 16 states,
+// issue and latency (62% of its slots with 14 warps an SM); 217 us for 4 x 1024 channels of 2048 steps, 16 states,
 // bf16.
 //
 // A lane holds eight steps of one channel; eight lanes are a channel's 64-step

@@ -6,9 +6,10 @@
 //
 // x at negative times comes from state_in (the last K - 1 inputs of the part
 // before, oldest first) or is zero.  The floor is bytes: one read of x and one
-// write of y (backward: x, dy, dx).  Measured in fp16 with four taps: 134 us for
-// 1 x 2560 x 65536 (5.0 TB/s, issue slots 63% busy), 10 us forward and 26 us
-// backward (62 instructions an element, bound by their issue) for 8 x 768 x 1024.
+// write of y (backward: x, dy, dx).  Measured in fp16 with four taps: 140 to 145 us for
+// 1 x 2560 x 65536 (4.6 to 4.8 TB/s, issue slots 63% busy), 10 us forward and 26 us
+// backward for 8 x 768 x 1024 (62 instructions an element at 51% of the issue slots:
+// a thread's next loads wait for its arithmetic), 178 us backward for 8 x 768 x 8192.
 #include "kernels.cuh"
 #include "rows.cuh"
 
@@ -421,10 +422,11 @@ cudaError_t launch_short_conv(const Rows& x, const float* w, const float* bias, 
 }
 
 // Parts of dw and dbias over the (batch row, vector) items of a channel: enough
-// blocks for every SM to hold four, each thread with at least one item.  One part
+// blocks for each of 148 SMs to hold four (592), each thread with at least one item.
+// (A number, not the device's count: the workspace's size is the same everywhere.)  One part
 // needs no second kernel: at 8 x 768 channels of 1024 steps in fp16, forward and
 // backward together take 28 us either way, and the call 22 us of the host's time
-// instead of 27.
+// instead of 27.  Longer rows were not measured with more parts.
 int short_conv_bwd_splits(int B, int H, int L) {
   const long long items = (long long)B * ((L + 7) / 8);
   const long long most = (items + kThreads - 1) / kThreads;
